@@ -5,6 +5,8 @@
  *
  *   copy_blocks             batched copy-on-write block copies (src -> dst);
  *   kv_swap_blocks          batched block moves to and from host memory;
+ *   kv_plan_step            block tables, slot mapping and lengths of a step, built
+ *                           on the GPU from the requests' lengths;
  *   kv_append               slot-mapped write of each new token's K and V row
  *                           (the pages' reshape-and-cache step);
  *   paged_attention_decode  single-query attention per sequence, reading K and
@@ -47,8 +49,8 @@
  *     out and the new K/V rows keep a 16-bit type.
  *   - Devices: a pool belongs to the device that was current when it was
  *     created; every call on it must be made with that device current.
- *   - Tracing: each call that enqueues work (kv_append, copy_blocks,
- *     kv_swap_blocks, the three decode calls, paged_attention_prefill) is one
+ *   - Tracing: each call that enqueues work (kv_plan_step, kv_append, copy_blocks,
+ *     kv_swap_blocks, the decode and prefill calls) is one
  *     NVTX range named after the call in the NVTX domain "pagedkv", opened on
  *     entry and closed on every return; with no profiling tool attached a
  *     range costs one pointer test.
@@ -92,6 +94,7 @@ typedef enum {
                                        num_tokens (the request is skipped), or a
                                        request with more than max_query_len queries
                                        (the queries past it are not computed)         */
+#define KV_DEVERR_NO_BLOCKS    0x80 /* kv_plan_step: the free list is too short          */
 
 typedef struct kv_pool* kv_pool_t;
 
@@ -149,6 +152,54 @@ kv_status kv_pool_create_quantized(int num_blocks, int block_size, int num_kv_he
 /* kv_pool_destroy -- free the handle and its error word (not the pools).
  * Work already queued with the handle must have finished.  NULL is a no-op. */
 kv_status kv_pool_destroy(kv_pool_t pool);
+
+/*
+ * kv_plan_step -- the bookkeeping of one step, on the GPU ("Part 3: single
+ * node", ch. 13 sec. 1: new tokens flattened into one stream with request
+ * boundaries, slots from the block table; "Lecture 3", sec. 3.1: a block is
+ * taken from the free list only when a request's last one is full).  What
+ * kv_append, paged_attention_decode and paged_attention_prefill then read is
+ * built from the requests' lengths without the host, so a captured step can
+ * grow its sequences.
+ *
+ * context_lens, new_lens: device int32 [batch]: tokens request b has cached,
+ *   and tokens it adds in this step (0: it waits).
+ * block_tables: device int32 [batch, max_blocks_per_seq], updated in place:
+ *   row b holds its ceil(context / block_size) blocks and gains the entries of
+ *   its new ones; no other entry is read or written.
+ * free_blocks: device int32 [num_free], block ids in the order they are handed
+ *   out; free_head: device int32 [1], how many of them are already taken.
+ *   Request 0's new blocks come first, then request 1's, ...
+ * free_head_out: device int32 [1]: free_head plus the blocks this step took.
+ * cu_seqlens: device int32 [batch + 1], seq_lens: device int32 [batch]
+ *   (context + new), slot_mapping: device int64 [num_tokens], positions: device
+ *   int32 [num_tokens] or NULL: token i of the stream goes to slot
+ *   slot_mapping[i] at position positions[i] of its request.  num_tokens is
+ *   the size of those arrays (>= the sum of new_lens; more for a captured step
+ *   of fixed size): entries past the last token get slot -1 (kv_append skips
+ *   it) and position 0.
+ * A request that cannot be placed keeps its length: seq_lens[b] =
+ *   context_lens[b], its tokens stay in the stream with slot -1, and its table
+ *   row is left alone.  That happens when its blocks run past num_free
+ *   (KV_DEVERR_NO_BLOCKS; from the first such request on, no request that
+ *   needs a block gets one), when it grows past its table row
+ *   (KV_DEVERR_SEQ_RANGE), or when its tokens run past num_tokens
+ *   (KV_DEVERR_QUERY_RANGE; cu_seqlens stops at num_tokens).  A negative length
+ *   counts as zero and sets KV_DEVERR_SEQ_RANGE; a table or free-list id
+ *   outside the pool gives slot -1 and sets KV_DEVERR_BLOCK_RANGE, as does a
+ *   free_head outside [0, num_free] (it is clamped).
+ * Inputs and outputs are distinct arrays (free_head and free_head_out,
+ *   context_lens / new_lens and seq_lens among them: KV_EINVAL).
+ * The pool gives block size and block count only; one launch, no workspace.
+ * Limits: 1 <= batch <= 4096, max_blocks_per_seq * block_size < 2^31.
+ * Errors: KV_EINVAL (null or misaligned pointer, bad size, the current device
+ *   is not the pool's), KV_EUNSUPPORTED (batch), KV_ECUDA.
+ */
+kv_status kv_plan_step(kv_pool_t pool, const int32_t* context_lens, const int32_t* new_lens,
+                       int batch, int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* free_blocks, int num_free, const int32_t* free_head,
+                       int32_t* free_head_out, int32_t* cu_seqlens, int32_t* seq_lens,
+                       int64_t* slot_mapping, int32_t* positions, int num_tokens, void* stream);
 
 /*
  * kv_append -- write each new token's K and V row into its slot

@@ -104,6 +104,12 @@ constexpr int kMaxGroups = 1024;   // cascade decode: groups per call
 // Record the text of a failed CUDA call for kv_last_cuda_error; returns KV_ECUDA.
 kv_status cuda_fail(cudaError_t e, const char* where);
 
+// Whether the calling thread's current device is the pool's.
+inline bool on_pool_device(const kv_pool& pool) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == pool.device;
+}
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (element
 // strides 1, no interleave, optional 128-byte swizzle, 256-byte L2 fills).
 bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, void* base,

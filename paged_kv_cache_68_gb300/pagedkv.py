@@ -7,7 +7,7 @@ fails, an exception is raised.
 
 The module-level functions carry the C names (``kv_pool_create``,
 ``kv_pool_create_quantized``,
-``kv_append``, ``copy_blocks``, ``kv_swap_blocks``, ``paged_attention_workspace_size``,
+``kv_plan_step``, ``kv_append``, ``copy_blocks``, ``kv_swap_blocks``, ``paged_attention_workspace_size``,
 ``paged_attention_decode``, ``paged_attention_cascade_workspace_size``,
 ``paged_attention_decode_cascade``, ``paged_attention_prefill``,
 ``paged_attention_decode_noalloc``,
@@ -20,7 +20,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -34,6 +34,7 @@ KV_DEVERR_SEQ_RANGE = 0x8
 KV_DEVERR_TIMEOUT = 0x10
 KV_DEVERR_GROUP_RANGE = 0x20
 KV_DEVERR_QUERY_RANGE = 0x40
+KV_DEVERR_NO_BLOCKS = 0x80
 
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 KV_FP8_E4M3, KV_INT8 = 3, 4
@@ -72,6 +73,7 @@ def load(build: bool = True) -> ctypes.CDLL:
             "kv_pool_create": ([I, I, I, I, I, P, P, ctypes.POINTER(P)], I),
             "kv_pool_create_quantized": ([I, I, I, I, I, I, P, P, P, P, F, F, ctypes.POINTER(P)], I),
             "kv_pool_destroy": ([P], I),
+            "kv_plan_step": ([P, P, P, I, P, I, P, I, P, P, P, P, P, P, I, P], I),
             "kv_append": ([P, P, P, P, I, P], I),
             "copy_blocks": ([P, P, I, P], I),
             "paged_attention_workspace_size": ([P, I, I, ctypes.POINTER(S)], I),
@@ -115,6 +117,25 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _same_device(*tensors) -> None:
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+
+
+def _shape(t, name: str, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A result tensor, allocated on the stream that writes it."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 # -- the C entry points, by name -----------------------------------------------
@@ -162,6 +183,44 @@ def kv_pool_create_quantized(k_codes: torch.Tensor, v_codes: torch.Tensor, dtype
 
 def kv_pool_destroy(handle) -> None:
     _check(load().kv_pool_destroy(handle), "kv_pool_destroy")
+
+
+class StepPlan(NamedTuple):
+    """What ``kv_plan_step`` writes beside the block tables."""
+    cu_seqlens: torch.Tensor      # int32 [batch + 1]
+    seq_lens: torch.Tensor        # int32 [batch]
+    slot_mapping: torch.Tensor    # int64 [num_tokens]
+    positions: torch.Tensor       # int32 [num_tokens]
+    free_head: torch.Tensor       # int32 [1]
+
+
+def kv_plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free_head,
+                 plan: StepPlan, stream=None) -> None:
+    """context_lens, new_lens int32 [B]; block_tables int32 [B, max_blocks]
+    (updated in place); free_blocks int32 [F], free_head int32 [1]; the results
+    go into ``plan``."""
+    _same_device(context_lens, new_lens, block_tables, free_blocks, free_head, *plan)
+    b, t = int(context_lens.numel()), int(plan.slot_mapping.numel())
+    _shape(new_lens, "new_lens", b)
+    _shape(context_lens, "context_lens", b)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError(f"block_tables must be [{b}, max_blocks]")
+    _shape(free_head, "free_head", 1)
+    _shape(plan.free_head, "plan.free_head", 1)
+    _shape(plan.cu_seqlens, "plan.cu_seqlens", b + 1)
+    _shape(plan.seq_lens, "plan.seq_lens", b)
+    if plan.positions is not None:
+        _shape(plan.positions, "plan.positions", t)
+    i32 = lambda x, n: _dev(x, n, torch.int32)
+    _check(load().kv_plan_step(
+        handle, i32(context_lens, "context_lens"), i32(new_lens, "new_lens"), b,
+        i32(block_tables, "block_tables"), int(block_tables.shape[1]),
+        i32(free_blocks, "free_blocks"), int(free_blocks.numel()), i32(free_head, "free_head"),
+        i32(plan.free_head, "plan.free_head"), i32(plan.cu_seqlens, "plan.cu_seqlens"),
+        i32(plan.seq_lens, "plan.seq_lens"),
+        _dev(plan.slot_mapping, "plan.slot_mapping", torch.int64),
+        None if plan.positions is None else i32(plan.positions, "plan.positions"), t,
+        _stream(stream)), "kv_plan_step")
 
 
 def kv_append(handle, k_new, v_new, slot_mapping, dtype, stream=None) -> None:
@@ -317,6 +376,22 @@ class KVPool:
             self.close()
         except Exception:
             pass
+
+    def plan_step(self, context_lens, new_lens, block_tables, free_blocks, free_head,
+                  num_tokens: int, out: Optional[StepPlan] = None, stream=None) -> StepPlan:
+        """Block tables (in place), slots, positions, offsets and lengths of one
+        step, built on the GPU; ``num_tokens`` sizes the token arrays."""
+        if out is None:
+            dev, b = context_lens.device, int(context_lens.numel())
+            new = lambda n, dt: _new((n,), dt, dev, stream)
+            out = StepPlan(new(b + 1, torch.int32), new(b, torch.int32),
+                           new(num_tokens, torch.int64), new(num_tokens, torch.int32),
+                           new(1, torch.int32))
+        elif int(out.slot_mapping.numel()) != num_tokens:
+            raise ValueError(f"out.slot_mapping must hold {num_tokens} tokens")
+        kv_plan_step(self.handle, context_lens, new_lens, block_tables, free_blocks, free_head, out,
+                     stream)
+        return out
 
     def append(self, k_new, v_new, slot_mapping, stream=None) -> None:
         kv_append(self.handle, k_new, v_new, slot_mapping, self.dtype, stream)
