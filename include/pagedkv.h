@@ -149,6 +149,43 @@ kv_status kv_pool_create_quantized(int num_blocks, int block_size, int num_kv_he
                                    void* k_pool, void* v_pool, float* k_scales, float* v_scales,
                                    float k_scale, float v_scale, kv_pool_t* out);
 
+/*
+ * kv_pool_create_block_scaled -- describe an 8-bit KV block pool with one scale
+ * for each (block, KV head) ("Part 3: single node", ch. 10: a scale for a group
+ * of values, kept beside their codes): the range follows the data as INT8's
+ * token scales do, at 8 bytes per block and head instead of per token, for FP8
+ * codes as well.
+ *
+ * cache_dtype, dtype, k_pool, v_pool: as for kv_pool_create_quantized.
+ * k_scales, v_scales: device fp32 [num_blocks, num_kv_heads], 16-byte aligned,
+ *   owned by the caller.  value = code * scale.
+ * kv_append decides the scales.  Let `rows` be the rows of a block that one
+ *   call writes, for one KV head and for K or V; qmax = 448 (KV_FP8_E4M3) or
+ *   127 (KV_INT8).  All arithmetic is fp32, each step rounded to nearest:
+ *     a = max |x| over the rows; old = the stored scale, or 0 when row 0 is one
+ *     of the rows (the block starts anew);
+ *     new = max(old, a / qmax), and 0 if that is below 2^-126;
+ *     a row written: code = Q(x * (1 / new)) (0 when new is 0);
+ *     a row not written, if new > old > 0: code = Q(code * (old / new)).
+ *   Q rounds to nearest even and saturates (448, 127).  FP8: infinities and
+ *   NaN do not count in a; an infinity saturates and NaN stays NaN.  INT8: a
+ *   row holding either gives the block and head the scale NaN, with codes 0 for
+ *   the call's rows, until the block starts anew.
+ *   The first write to a block must therefore include its row 0 (as appending
+ *   in order does), or find its scales initialised.
+ *   Calls that write into the same block must not overlap in time.
+ * copy_blocks and kv_swap_blocks move scales with the codes (host scales
+ *   [num_host_blocks, num_kv_heads]); decode and prefill, scored or not, read
+ *   them; paged_attention_decode_cascade decodes plainly.
+ * The handle allocates 4 bytes of device memory per token slot and per block
+ *   beside the error word (kv_append's notes of which row goes where).
+ * Limits and errors: those of kv_pool_create_quantized.
+ */
+kv_status kv_pool_create_block_scaled(int num_blocks, int block_size, int num_kv_heads,
+                                      int head_dim, kv_dtype cache_dtype, kv_dtype dtype,
+                                      void* k_pool, void* v_pool, float* k_scales, float* v_scales,
+                                      kv_pool_t* out);
+
 /* kv_pool_destroy -- free the handle and its error word (not the pools).
  * Work already queued with the handle must have finished.  NULL is a no-op. */
 kv_status kv_pool_destroy(kv_pool_t pool);
@@ -240,8 +277,9 @@ kv_status copy_blocks(kv_pool_t pool, const int32_t* pairs, int num_pairs, void*
  *   pool's element type (codes for an 8-bit pool), 16-byte aligned, in pinned
  *   host memory the device can address (cudaHostAlloc / cudaHostRegister, or
  *   managed memory); the kernel reads or writes it directly.
- * host_k_scales, host_v_scales: INT8 pools only, fp32 [num_host_blocks,
- *   num_kv_heads, block_size] in the same kind of memory; NULL otherwise.
+ * host_k_scales, host_v_scales: INT8 pools, fp32 [num_host_blocks,
+ *   num_kv_heads, block_size], and block-scaled pools, fp32 [num_host_blocks,
+ *   num_kv_heads], in the same kind of memory; NULL otherwise.
  * pairs: int32 [num_pairs, 2] = (pool block, host block), device-accessible.
  *   KV_SWAP_OUT: host[h] <- pool[g]; KV_SWAP_IN: pool[g] <- host[h], codes and
  *   scales alike.  Precondition: destination blocks are distinct and no
@@ -308,13 +346,71 @@ kv_status paged_attention_decode_launches(kv_pool_t pool, int batch, int num_q_h
  *   data) is taken for a live count only if it matches that tag, with
  *   probability 2^-64.  Calls that use the same workspace must not overlap
  *   in time.
- * Errors: KV_EINVAL, KV_EUNSUPPORTED, KV_ENOWORKSPACE, KV_ECUDA.
+ * Errors: KV_EINVAL, KV_EUNSUPPORTED (also a block size whose K and V tiles do
+ *   not fit shared memory, e.g. 256), KV_ENOWORKSPACE, KV_ECUDA.
  */
 kv_status paged_attention_decode(kv_pool_t pool, const void* q, void* out,
                                  const int32_t* block_tables, int max_blocks_per_seq,
                                  const int32_t* seq_lens, int batch, int num_q_heads,
                                  float scale, int num_kv_heads, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * kv_score_mods -- what scored attention does to a score before the softmax,
+ * and which positions a query sees.  A query at position P (decode: L - 1) of
+ * request b, query head h:
+ *     s_t = scale * dot(q, K_t)
+ *     s_t = softcap * tanh(s_t / softcap)            if softcap > 0
+ *     s_t = s_t - alibi_slopes[h] * |P - t|          if alibi_slopes
+ * over the positions t that pass every mask given:
+ *     t <= P, or t < min(prefix_lens[b], L)          (causal, prefix mask)
+ *     t >  P - window                                if window > 0
+ *     t >= first_visible[query]                      (document mask: the first
+ *                                                     position of its document)
+ * A query that sees nothing gives zeros.
+ *
+ * softcap: >= 0, finite; 0 = none.  window: >= 0; 0 = none.
+ * alibi_slopes: device fp32 [num_q_heads], finite, or NULL.
+ * first_visible: device int32, decode [batch], prefill [num_tokens], or NULL;
+ *   values below 0 count as 0.
+ * prefix_lens: prefill only, device int32 [batch], or NULL (decode: NULL).
+ *   Positions below the prefix length are seen by every query of the request,
+ *   also by earlier ones; they must have been appended, so a prefix lies in the
+ *   first chunk or before it.
+ * K and V of a position that no query of the request sees may hold anything
+ *   (infinities and NaN included) if that holds for decode; in prefill a
+ *   position that some query of the request sees must hold finite values.
+ */
+typedef struct {
+    float softcap;
+    const float* alibi_slopes;
+    int window;
+    const int32_t* first_visible;
+    const int32_t* prefix_lens;
+} kv_score_mods;
+
+/*
+ * paged_attention_scored_workspace_size -- bytes of device workspace that
+ * paged_attention_decode_scored needs for this pool, batch and head count.
+ */
+kv_status paged_attention_scored_workspace_size(kv_pool_t pool, int batch, int num_q_heads,
+                                                size_t* bytes);
+
+/*
+ * paged_attention_decode_scored -- paged_attention_decode with capped or
+ * biased scores and masks (`mods`, host memory, read by the call; see
+ * kv_score_mods).  Blocks wholly before the first visible position are not
+ * read.  Every pool kind and shape of paged_attention_decode; the other
+ * arguments, limits, errors and device error bits are its own, with
+ * paged_attention_scored_workspace_size for the workspace.  KV_EINVAL also for
+ * mods NULL or out of range, prefix_lens given, or a current device that is
+ * not the pool's.
+ */
+kv_status paged_attention_decode_scored(kv_pool_t pool, const void* q, void* out,
+                                        const int32_t* block_tables, int max_blocks_per_seq,
+                                        const int32_t* seq_lens, int batch, int num_q_heads,
+                                        float scale, int num_kv_heads, const kv_score_mods* mods,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * paged_attention_cascade_workspace_size -- bytes of workspace that
@@ -411,6 +507,21 @@ kv_status paged_attention_prefill(kv_pool_t pool, const void* q, void* out,
                                   const int32_t* block_tables, int max_blocks_per_seq,
                                   const int32_t* seq_lens, int batch, int num_q_heads,
                                   float scale, int num_kv_heads, void* stream);
+
+/*
+ * paged_attention_prefill_scored -- paged_attention_prefill with capped or
+ * biased scores and masks (`mods`, host memory, read by the call; see
+ * kv_score_mods).  KV tiles that no query of a tile pair sees are not read.
+ * The other arguments, limits, errors and device error bits are those of
+ * paged_attention_prefill.  KV_EINVAL also for mods NULL or out of range, or a
+ * current device that is not the pool's.
+ */
+kv_status paged_attention_prefill_scored(kv_pool_t pool, const void* q, void* out,
+                                         const int32_t* cu_seqlens, int num_tokens,
+                                         int max_query_len, const int32_t* block_tables,
+                                         int max_blocks_per_seq, const int32_t* seq_lens,
+                                         int batch, int num_q_heads, float scale, int num_kv_heads,
+                                         const kv_score_mods* mods, void* stream);
 
 /*
  * paged_attention_decode_noalloc -- paged_attention_decode without a

@@ -126,12 +126,34 @@ kv_status cuda_fail(cudaError_t e, const char* where) {
     return KV_ECUDA;
 }
 
-cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups,
+// The decode kernels of a pool: their dispatch and occupancy entry points.
+struct DecodeUnit {
+    cudaError_t (*dispatch)(const kv_pool&, const DecodeCall&, const DecodePlan&, cudaStream_t);
+    cudaError_t (*attrs)(const kv_pool&, int, size_t, int*);
+};
+static DecodeUnit decode_unit(const kv_pool& pool, bool scored) {
+#define PKV_UNIT(name) DecodeUnit{decode_dispatch_##name, decode_attrs_##name}
+    const bool bf = pool.dtype == KV_BF16;
+    if (pool.block_scales) {
+        if (scored) return bf ? PKV_UNIT(scored_block_bf16) : PKV_UNIT(scored_block_f16);
+        return bf ? PKV_UNIT(block_bf16) : PKV_UNIT(block_f16);
+    }
+    if (is_q8(pool)) {
+        if (scored) return bf ? PKV_UNIT(scored_q8_bf16) : PKV_UNIT(scored_q8_f16);
+        return bf ? PKV_UNIT(q8_bf16) : PKV_UNIT(q8_f16);
+    }
+    if (pool.dtype == KV_F32) return scored ? PKV_UNIT(scored_f32) : PKV_UNIT(f32);
+    if (scored) return bf ? PKV_UNIT(scored_bf16) : PKV_UNIT(scored_f16);
+    return bf ? PKV_UNIT(bf16) : PKV_UNIT(f16);
+#undef PKV_UNIT
+}
+
+cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups, bool scored,
                         DecodePlan* plan) {
     {
         std::lock_guard<std::mutex> lock(pool.plan_mu);
         if (pool.plan_batch == batch && pool.plan_hq == num_q_heads &&
-            pool.plan_groups == num_groups) {
+            pool.plan_groups == num_groups && pool.plan_scored == scored) {
             *plan = pool.plan;
             return cudaSuccess;
         }
@@ -145,8 +167,10 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
     const bool pairs = q8 ? dec::q8_pairs_blocks(pool, G)
                           : pool.block_size == 8 && dec::use_tensor_cores(pool, G);
     const int bs = pool.block_size * (pairs ? 2 : 1);
-    const int sb = pool.cache_dtype == KV_INT8 ? 4 : 0;     // scale bytes per tile row
-    const size_t stage = 2ull * bs * D * elt + 2ull * bs * sb;
+    // scale bytes per tile row, or per stage
+    const int sb = pool.cache_dtype == KV_INT8 && !pool.block_scales ? 4 : 0;
+    const int stage_sb = pool.block_scales ? dec::kStageScales : 0;
+    const size_t stage = 2ull * bs * D * elt + 2ull * bs * sb + stage_sb;
     // Ring depth S is a multiple of the consumer-warp count (each stage has a
     // fixed consumer).  Pick the S with the most (resident CTAs x stages per
     // warp, the latter counted up to max_per_warp), then the deepest ring.
@@ -155,24 +179,18 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
     // a third stage per warp pays even at one CTA fewer per SM (Llama-3-8B
     // step 0.2036 -> 0.1932 ms); 16-bit and FP8 pools run faster with three
     // CTAs of two stages per warp (0.1854 -> 0.1898 ms FP8, 0.2844 -> 0.2879 bf16).
-    const int max_per_warp = pool.cache_dtype == KV_INT8 ? 3 : 2;
+    const int max_per_warp = sb ? 3 : 2;
+    const DecodeUnit unit = decode_unit(pool, scored);
     int best_s = 0, best_occ = 0, best_score = -1;
     size_t best_smem = 0;
     for (int S = ncw; S <= 8 * ncw; S += ncw) {
         if (S > ncw && (size_t)S * stage > kMaxRingBytes) break;
         // + 1 KB: the kernel rounds its shared-memory base up to 1 KB
-        const size_t smem = dec::Layout(S, batch, bs, G, D, elt, num_groups, sb).total + 1024;
+        const size_t smem =
+            dec::Layout(S, batch, bs, G, D, elt, num_groups, sb, stage_sb, scored).total + 1024;
         if (smem > kMaxSmem) break;
         int occ = 0;
-        cudaError_t e = cudaErrorNotSupported;
-        if (q8) {
-            if (pool.dtype == KV_F16) e = decode_attrs_q8_f16(pool, G, smem, &occ);
-            if (pool.dtype == KV_BF16) e = decode_attrs_q8_bf16(pool, G, smem, &occ);
-        } else {
-            if (pool.dtype == KV_F32) e = decode_attrs_f32(pool, G, smem, &occ);
-            if (pool.dtype == KV_F16) e = decode_attrs_f16(pool, G, smem, &occ);
-            if (pool.dtype == KV_BF16) e = decode_attrs_bf16(pool, G, smem, &occ);
-        }
+        const cudaError_t e = unit.attrs(pool, G, smem, &occ);
         if (e != cudaSuccess) return e;
         const int per_warp = S / ncw > max_per_warp ? max_per_warp : S / ncw;
         const int score = occ * per_warp;
@@ -205,6 +223,7 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
         pool.plan_batch = batch;
         pool.plan_hq = num_q_heads;
         pool.plan_groups = num_groups;
+        pool.plan_scored = scored;
     }
     *plan = pl;
     return cudaSuccess;
@@ -212,17 +231,7 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
 
 cudaError_t launch_decode(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
                           cudaStream_t stream) {
-    if (is_q8(pool)) {
-        if (pool.dtype == KV_F16) return decode_dispatch_q8_f16(pool, call, plan, stream);
-        if (pool.dtype == KV_BF16) return decode_dispatch_q8_bf16(pool, call, plan, stream);
-        return cudaErrorNotSupported;
-    }
-    switch (pool.dtype) {
-        case KV_F32: return decode_dispatch_f32(pool, call, plan, stream);
-        case KV_F16: return decode_dispatch_f16(pool, call, plan, stream);
-        case KV_BF16: return decode_dispatch_bf16(pool, call, plan, stream);
-    }
-    return cudaErrorNotSupported;
+    return decode_unit(pool, call.mods != nullptr).dispatch(pool, call, plan, stream);
 }
 
 }  // namespace pagedkv
@@ -304,6 +313,35 @@ kv_status kv_pool_create_quantized(int num_blocks, int block_size, int num_kv_he
     return finish_pool(p, out);
 }
 
+kv_status kv_pool_create_block_scaled(int num_blocks, int block_size, int num_kv_heads,
+                                      int head_dim, kv_dtype cache_dtype, kv_dtype dtype,
+                                      void* k_pool, void* v_pool, float* k_scales, float* v_scales,
+                                      kv_pool_t* out) {
+    if (!out) return KV_EINVAL;
+    *out = nullptr;
+    if (cache_dtype != KV_FP8_E4M3 && cache_dtype != KV_INT8) return KV_EUNSUPPORTED;
+    if (dtype != KV_F16 && dtype != KV_BF16) return KV_EUNSUPPORTED;
+    if (head_dim != 128 || block_size % 16 != 0) return KV_EUNSUPPORTED;
+    kv_status st = check_geometry(num_blocks, block_size, num_kv_heads, k_pool, v_pool);
+    if (st != KV_OK) return st;
+    if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) return KV_EINVAL;
+    kv_pool* p = new (std::nothrow) kv_pool();
+    if (!p) return KV_EINVAL;
+    p->num_blocks = num_blocks;
+    p->block_size = block_size;
+    p->num_kv_heads = num_kv_heads;
+    p->head_dim = head_dim;
+    p->dtype = dtype;
+    p->cache_dtype = cache_dtype;
+    p->elem_bytes = 1;
+    p->k = k_pool;
+    p->v = v_pool;
+    p->k_scales = k_scales;
+    p->v_scales = v_scales;
+    p->block_scales = true;
+    return finish_pool(p, out);
+}
+
 // Device, error word and tensor maps of a filled-in pool; frees it on failure.
 static kv_status finish_pool(kv_pool* p, kv_pool_t* out) {
     const int head_dim = p->head_dim, block_size = p->block_size;
@@ -314,8 +352,18 @@ static kv_status finish_pool(kv_pool* p, kv_pool_t* out) {
         e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
     if (e == cudaSuccess) e = cudaMalloc(&p->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(p->d_err, 0, sizeof(int));
+    if (e == cudaSuccess && p->block_scales) {
+        const size_t rows = (size_t)p->num_blocks * p->block_size;
+        const size_t bytes = sizeof(int) * (rows + p->num_blocks);
+        e = cudaMalloc(&p->d_owner, bytes);
+        if (e == cudaSuccess) {
+            p->d_leader = p->d_owner + rows;
+            e = cudaMemset(p->d_owner, 0, bytes);
+        }
+    }
     if (e != cudaSuccess) {
-        if (p->d_err) cudaFree(p->d_err);
+        cudaFree(p->d_err);
+        cudaFree(p->d_owner);
         delete p;
         return pagedkv::cuda_fail(e, "kv_pool_create");
     }
@@ -335,6 +383,7 @@ static kv_status finish_pool(kv_pool* p, kv_pool_t* out) {
                          encode_pool_map_h2(&p->tmap_v_h2, v_pool, *p);
     if (!maps_ok) {
         cudaFree(p->d_err);
+        cudaFree(p->d_owner);
         delete p;
         std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
                       "kv_pool_create: cuTensorMapEncodeTiled failed");
@@ -347,6 +396,8 @@ static kv_status finish_pool(kv_pool* p, kv_pool_t* out) {
 kv_status kv_pool_destroy(kv_pool_t pool) {
     if (!pool) return KV_OK;
     cudaError_t e = cudaFree(pool->d_err);
+    const cudaError_t e2 = cudaFree(pool->d_owner);
+    if (e == cudaSuccess) e = e2;
     delete pool;
     return e == cudaSuccess ? KV_OK : pagedkv::cuda_fail(e, "kv_pool_destroy");
 }
@@ -399,7 +450,7 @@ kv_status kv_swap_blocks(kv_pool_t pool, void* host_k, void* host_v, float* host
         !device_accessible(host_k) || !device_accessible(host_v))
         return KV_EINVAL;
     if ((long long)num_host_blocks * pool->block_size >= (1ll << 31)) return KV_EINVAL;
-    if (pool->cache_dtype == KV_INT8) {
+    if (pool->k_scales) {
         if (!host_k_scales || !host_v_scales || !aligned16(host_k_scales) ||
             !aligned16(host_v_scales) || !device_accessible(host_k_scales) ||
             !device_accessible(host_v_scales))
@@ -429,7 +480,7 @@ kv_status paged_attention_workspace_size(kv_pool_t pool, int batch, int num_q_he
     kv_status st = check_decode_shape(pool, batch, num_q_heads);
     if (st != KV_OK) return st;
     pagedkv::DecodePlan plan;
-    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, 0, &plan);
+    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, 0, false, &plan);
     if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
     if (e != cudaSuccess) return pagedkv::cuda_fail(e, "paged_attention_workspace_size");
     *bytes = plan.ws_bytes;
@@ -442,7 +493,7 @@ kv_status paged_attention_decode_launches(kv_pool_t pool, int batch, int num_q_h
     kv_status st = check_decode_shape(pool, batch, num_q_heads);
     if (st != KV_OK) return st;
     pagedkv::DecodePlan plan;
-    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, 0, &plan);
+    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, 0, false, &plan);
     if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
     if (e != cudaSuccess) return pagedkv::cuda_fail(e, "paged_attention_decode_launches");
     *launches = 1 + (pagedkv::merge_warps_per_pair(plan.num_ctas * pagedkv::dec::NCW,
@@ -456,7 +507,8 @@ static kv_status decode_impl(kv_pool_t pool, const void* q, void* out,
                              int num_kv_heads, void* workspace, size_t workspace_bytes,
                              const int32_t* g_first, const int32_t* g_size,
                              const int32_t* g_blocks, int num_groups, const float* pst_o,
-                             const float* pst_lse, unsigned long long tag, void* stream) {
+                             const float* pst_lse, unsigned long long tag, void* stream,
+                             const kv_score_mods* mods = nullptr) {
     kv_status st = check_decode_shape(pool, batch, num_q_heads);
     if (st != KV_OK) return st;
     if (num_kv_heads != pool->num_kv_heads) return KV_EINVAL;
@@ -470,7 +522,8 @@ static kv_status decode_impl(kv_pool_t pool, const void* q, void* out,
         return KV_EUNSUPPORTED;
     if (!(scale == scale)) return KV_EINVAL;
     pagedkv::DecodePlan plan;
-    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, num_groups, &plan);
+    cudaError_t e =
+        pagedkv::plan_decode(*pool, batch, num_q_heads, num_groups, mods != nullptr, &plan);
     if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
     if (e != cudaSuccess) return pagedkv::cuda_fail(e, "paged_attention_decode(plan)");
     if (workspace_bytes < plan.ws_bytes) return KV_ENOWORKSPACE;
@@ -483,6 +536,7 @@ static kv_status decode_impl(kv_pool_t pool, const void* q, void* out,
     call.num_groups = num_groups;
     call.pst_o = pst_o;
     call.pst_lse = pst_lse;
+    call.mods = mods;
     e = pagedkv::launch_decode(*pool, call, plan, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KV_OK : pagedkv::cuda_fail(e, "paged_attention_decode");
 }
@@ -496,6 +550,33 @@ kv_status paged_attention_decode(kv_pool_t pool, const void* q, void* out,
     return decode_impl(pool, q, out, block_tables, max_blocks_per_seq, seq_lens, batch,
                        num_q_heads, scale, num_kv_heads, workspace, workspace_bytes, nullptr,
                        nullptr, nullptr, 0, nullptr, nullptr, 0, stream);
+}
+
+kv_status paged_attention_scored_workspace_size(kv_pool_t pool, int batch, int num_q_heads,
+                                                size_t* bytes) {
+    if (!bytes) return KV_EINVAL;
+    kv_status st = check_decode_shape(pool, batch, num_q_heads);
+    if (st != KV_OK) return st;
+    pagedkv::DecodePlan plan;
+    cudaError_t e = pagedkv::plan_decode(*pool, batch, num_q_heads, 0, true, &plan);
+    if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
+    if (e != cudaSuccess) return pagedkv::cuda_fail(e, "paged_attention_scored_workspace_size");
+    *bytes = plan.ws_bytes;
+    return KV_OK;
+}
+
+kv_status paged_attention_decode_scored(kv_pool_t pool, const void* q, void* out,
+                                        const int32_t* block_tables, int max_blocks_per_seq,
+                                        const int32_t* seq_lens, int batch, int num_q_heads,
+                                        float scale, int num_kv_heads, const kv_score_mods* mods,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    const pagedkv::NvtxRange range("paged_attention_decode_scored");
+    if (!pool || !pagedkv::mods_ok(mods) || mods->prefix_lens) return KV_EINVAL;
+    if ((long long)max_blocks_per_seq * pool->block_size >= (1ll << 31)) return KV_EINVAL;
+    if (!pagedkv::on_pool_device(*pool)) return KV_EINVAL;
+    return decode_impl(pool, q, out, block_tables, max_blocks_per_seq, seq_lens, batch,
+                       num_q_heads, scale, num_kv_heads, workspace, workspace_bytes, nullptr,
+                       nullptr, nullptr, 0, nullptr, nullptr, 0, stream, mods);
 }
 
 kv_status kv_pool_set_wait_limit(kv_pool_t pool, unsigned long long limit_ns) {

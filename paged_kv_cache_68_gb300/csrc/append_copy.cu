@@ -163,12 +163,24 @@ __global__ void __launch_bounds__(256) append_q8_kernel(
 }
 
 // One CTA per (pair, array): a whole block of one of the pool's arrays (K, V
-// and, for INT8 pools, the K and V scales), blk16[a] = its block bytes / 16.
+// and, for INT8 and block-scaled pools, the K and V scales), blk16[a] = its
+// block bytes / 16; words > 0: arrays 2 and 3 hold that many 4-byte words per
+// block instead (block scales: a block's num_kv_heads scales need not be a
+// multiple of 16 bytes).
 struct CopyArrays {
     uint4* base[4];
     int blk16[4];
     int n;
+    int words;
 };
+
+// The words of one block of a scale array, by one CTA.
+__device__ __forceinline__ void copy_words(const uint4* src, uint4* dst, size_t s, size_t d,
+                                           int words) {
+    const uint32_t* sw = reinterpret_cast<const uint32_t*>(src) + s * words;
+    uint32_t* dw = reinterpret_cast<uint32_t*>(dst) + d * words;
+    for (int i = threadIdx.x; i < words; i += 256) dw[i] = sw[i];
+}
 
 __global__ void __launch_bounds__(256) copy_blocks_kernel(
     const int32_t* __restrict__ pairs, int num_pairs, CopyArrays arrays, int num_blocks,
@@ -181,6 +193,10 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(
     const int src = pairs[2 * pair], dst = pairs[2 * pair + 1];
     if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
         if (threadIdx.x == 0 && a == 0) atomicOr(err, KV_DEVERR_PAIR_RANGE);
+        return;
+    }
+    if (a >= 2 && arrays.words > 0) {
+        copy_words(arrays.base[a], arrays.base[a], src, dst, arrays.words);
         return;
     }
     const int blk16 = arrays.blk16[a];
@@ -209,6 +225,7 @@ struct SwapArrays {
     uint4* host[4];
     int blk16[4];
     int n;
+    int words;                    // as in CopyArrays
 };
 
 __global__ void __launch_bounds__(256) swap_blocks_kernel(
@@ -222,6 +239,11 @@ __global__ void __launch_bounds__(256) swap_blocks_kernel(
     const int g = pairs[2 * pair], h = pairs[2 * pair + 1];
     if (g < 0 || g >= num_gpu_blocks || h < 0 || h >= num_host_blocks) {
         if (threadIdx.x == 0 && a == 0) atomicOr(err, KV_DEVERR_PAIR_RANGE);
+        return;
+    }
+    if (a >= 2 && arrays.words > 0) {
+        if (to_host) copy_words(arrays.gpu[a], arrays.host[a], g, h, arrays.words);
+        else copy_words(arrays.host[a], arrays.gpu[a], h, g, arrays.words);
         return;
     }
     const int blk16 = arrays.blk16[a];
@@ -264,6 +286,8 @@ void pdl_attr(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr) {
 cudaError_t launch_append(const kv_pool& pool, const void* k_new, const void* v_new,
                           const int64_t* slots, int num_tokens, cudaStream_t stream) {
     if (num_tokens <= 0) return cudaSuccess;
+    if (pool.block_scales)
+        return launch_append_block_scaled(pool, k_new, v_new, slots, num_tokens, stream);
     if (is_q8(pool)) {
         const long long warps = 2ll * num_tokens;
         const int grid = (int)((warps * 32 + 255) / 256);
@@ -302,10 +326,11 @@ cudaError_t launch_copy_blocks(const kv_pool& pool, const int32_t* pairs, int nu
     arr.base[1] = static_cast<uint4*>(pool.v);
     arr.blk16[0] = arr.blk16[1] = blk16;
     arr.n = 2;
-    if (pool.cache_dtype == KV_INT8) {
+    if (pool.k_scales) {
         arr.base[2] = reinterpret_cast<uint4*>(pool.k_scales);
         arr.base[3] = reinterpret_cast<uint4*>(pool.v_scales);
         arr.blk16[2] = arr.blk16[3] = pool.block_size * pool.num_kv_heads * 4 / 16;
+        arr.words = pool.block_scales ? pool.num_kv_heads : 0;
         arr.n = 4;
     }
     if ((long long)arr.n * num_pairs > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -329,12 +354,13 @@ cudaError_t launch_swap_blocks(const kv_pool& pool, void* host_k, void* host_v,
     arr.host[1] = static_cast<uint4*>(host_v);
     arr.blk16[0] = arr.blk16[1] = blk16;
     arr.n = 2;
-    if (pool.cache_dtype == KV_INT8) {
+    if (pool.k_scales) {
         arr.gpu[2] = reinterpret_cast<uint4*>(pool.k_scales);
         arr.gpu[3] = reinterpret_cast<uint4*>(pool.v_scales);
         arr.host[2] = reinterpret_cast<uint4*>(host_k_scales);
         arr.host[3] = reinterpret_cast<uint4*>(host_v_scales);
         arr.blk16[2] = arr.blk16[3] = pool.block_size * pool.num_kv_heads * 4 / 16;
+        arr.words = pool.block_scales ? pool.num_kv_heads : 0;
         arr.n = 4;
     }
     if ((long long)arr.n * num_pairs > 0x7fffffffll) return cudaErrorInvalidValue;

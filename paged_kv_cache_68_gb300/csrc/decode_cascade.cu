@@ -35,7 +35,7 @@ struct PrefixPlan {
 // the grids can differ), given the plain plan's need in *bytes.
 kv_status split_part(kv_pool* pool, int batch, int num_q_heads, int num_groups, size_t* bytes) {
     DecodePlan dp;
-    cudaError_t e = plan_decode(*pool, batch, num_q_heads, num_groups, &dp);
+    cudaError_t e = plan_decode(*pool, batch, num_q_heads, num_groups, false, &dp);
     if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
     if (e != cudaSuccess) return cuda_fail(e, "paged_attention_decode_cascade(plan)");
     if (dp.ws_bytes > *bytes) *bytes = dp.ws_bytes;
@@ -44,10 +44,11 @@ kv_status split_part(kv_pool* pool, int batch, int num_q_heads, int num_groups, 
 
 // The shapes with a prefix kernel: head_dim 128, groups of 1, 2, 4 or 8, block
 // size 16 or 32, a pool with 128-byte-swizzled tensor maps; 16-bit pools, and
-// 8-bit pools with 16-bit queries.
+// 8-bit pools with pool or token scales and 16-bit queries.
 bool cascade_shape(const kv_pool& pool, int group) {
     if (pool.head_dim != 128 || !(group == 1 || group == 2 || group == 4 || group == 8) ||
-        !(pool.block_size == 16 || pool.block_size == 32) || !pool.has_swizzled_maps)
+        !(pool.block_size == 16 || pool.block_size == 32) || !pool.has_swizzled_maps ||
+        pool.block_scales)
         return false;
     if (is_q8(pool)) return pool.dtype == KV_BF16 || pool.dtype == KV_F16;
     return pool.elem_bytes == 2;

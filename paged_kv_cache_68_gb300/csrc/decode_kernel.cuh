@@ -103,6 +103,13 @@ struct Params {
     // split kernel by the warp that finishes last; > 0 = merged by
     // paged_decode_merge, that many warps per (b, g) (they split its partials)
     int merge_wpp;
+    // Scored decode (policies with kMod): the cap (0: none), its reciprocal,
+    // the heads' slopes (null: none), the window (0: none) and the first
+    // visible position of each sequence (null: 0)
+    float softcap, inv_softcap;
+    const float* slopes;     // [num_q_heads]
+    int window;
+    const int32_t* first;    // [batch]
 };
 
 // ---------------------------------------------------------------- layout ---
@@ -110,22 +117,25 @@ struct Layout {
     uint32_t full, valid, misc, prefix, groups, skip, pst, pbuf, abuf, sring, ring;
     uint32_t pst_bytes, tx_bytes, stage_bytes, total;
     // elt: bytes per pool element; K: cascade groups (0 for plain decode);
-    // sb: scale bytes per token row of a tile (INT8 pools: 4)
-    __host__ __device__ Layout(int S, int B, int bs, int G, int D, int elt, int K = 0, int sb = 0) {
+    // sb: scale bytes per token row of a tile (INT8 pools: 4); stage_sb: scale
+    // bytes per stage (block-scaled pools: kStageScales); skips: the leading
+    // units each sequence skips are kept (scored decode)
+    __host__ __device__ Layout(int S, int B, int bs, int G, int D, int elt, int K = 0, int sb = 0,
+                               int stage_sb = 0, bool skips = false) {
         uint32_t off = 0;
         full = off;   off += 8u * S;
         valid = off;  off += 4u * S;
         misc = off;   off += 4u * 40;            // abort flag + warp totals
         prefix = off; off += 4u * (B + 1);
         groups = off; off += K > 0 ? 4u * 3u * K : 0u;   // used groups: first, size, blocks
-        skip = off;   off += K > 0 ? 4u * B : 0u;        // leading blocks each sequence skips
+        skip = off;   off += K > 0 || skips ? 4u * B : 0u;   // leading units each sequence skips
         off = (off + 15u) & ~15u;
         pst_bytes = K > 0 ? (4u * G * D + 4u * G + 15u) & ~15u : 0u;
         pst = off;    off += NCW * pst_bytes;    // prefix state, one per warp
         pbuf = off;   off += 8u * NCW * bs * G;
         abuf = off;   off += 8u * NCW * G;
         off = (off + 15u) & ~15u;
-        sring = off;  off += (uint32_t)S * 2u * bs * sb;  // per stage: K then V scales
+        sring = off;  off += (uint32_t)S * (2u * bs * sb + stage_sb);  // per stage: K then V scales
         off = (off + 1023u) & ~1023u;              // swizzle atoms are 1 KB
         ring = off;
         stage_bytes = (2u * bs * D * elt + 127u) & ~127u;   // K tile then V tile
@@ -265,6 +275,12 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // -- tensor-core helpers (16-bit operands, fp32 accumulate) --
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -340,6 +356,11 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
                  : "memory");
+}
+// This thread's cp.async copies so far count as one arrival on `bar` when
+// they have landed (an arrival the barrier's count already expects).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -543,7 +564,63 @@ __device__ __forceinline__ float fold_state(float M, float& den, float lse_p, fl
     return M2;
 }
 
-template <typename T, int D, int G, int BSC>
+// What scored decode does to a score, for the NH query heads a lane holds
+// scores of.  In base 2 (s log2 e, as the softmax takes it):
+//   cap > 0:  s <- cap tanh(s / cap) = cap (1 - 2 / (1 + exp(2 s / cap))):
+//     two MUFU operations a score (exp2, reciprocal), absolute error about
+//     2^-23 cap; the fp32 policy calls tanhf, whose error is relative;
+//   slopes:   s <- s - slope |P - t|, P = L - 1 the query's position: t <= P,
+//     so the bias is slope (t - P), exact up to one rounding of the product;
+//   masks:    rows of the tile before n_lo, like rows from n_valid on, take no
+//     part.
+// Without kMod every member is unused and every call the identity.
+template <bool MOD, int NH, bool EXACT = false>
+struct ScoreMods {
+    float cap2, c1;            // cap log2 e; 2 / cap (0: no cap)
+    float slope2[NH];          // slope log2 e
+    float dist0;               // position of the unit's first row less P
+    int n_lo;                  // first visible row of the unit (may be <= 0)
+
+    // head(i): the i-th query head of this lane, or -1
+    template <class Head>
+    __device__ __forceinline__ void set(const Params& p, Head&& head) {
+        if constexpr (MOD) {
+            cap2 = p.softcap * 1.4426950408889634f;
+            c1 = 2.f * p.inv_softcap;
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                const int h = head(i);
+                slope2[i] = p.slopes != nullptr && h >= 0 ? p.slopes[h] * 1.4426950408889634f : 0.f;
+            }
+            dist0 = 0.f;
+            n_lo = 0;
+        }
+    }
+    __device__ __forceinline__ void unit(int lo, int dist) {
+        if constexpr (MOD) {
+            n_lo = lo;
+            dist0 = (float)dist;
+        }
+    }
+    __device__ __forceinline__ bool sees(int row) const {
+        if constexpr (MOD) return row >= n_lo;
+        else return true;
+    }
+    // y: the score of tile row `row` for the lane's head i, base 2
+    __device__ __forceinline__ float apply(float y, int row, int i) const {
+        if constexpr (MOD) {
+            if (c1 != 0.f) {
+                if constexpr (EXACT) y = cap2 * tanhf(y * (0.5f * c1 * 0.6931471805599453f));
+                else y = fmaf(-2.f * cap2, fast_rcp(1.f + fast_exp2(y * c1)), cap2);
+            }
+            return fmaf(slope2[i], dist0 + (float)row, y);
+        } else {
+            return y;
+        }
+    }
+};
+
+template <typename T, int D, int G, int BSC, bool MOD = false>
 struct CorePolicy {
     using C = Cfg<T, D, G>;
     static constexpr bool kSwizzled = false;
@@ -551,8 +628,11 @@ struct CorePolicy {
     static constexpr int kMinBlocks = G >= 8 ? 2 : (G >= 4 ? 3 : 4);
     static constexpr int kKvBytes = sizeof(T);   // pool element
     static constexpr int kScaleBytes = 0;
+    static constexpr bool kBlockScales = false;
+    static constexpr bool kMod = MOD;
     static constexpr int kUnitBlocks = 1;        // pool blocks per work unit
 
+    ScoreMods<MOD, 1, std::is_same<T, float>::value> mods;
     float2* pb;                   // this warp's (score | p, p) [bs][G]
     float2* ab;                   // this warp's (alpha, alpha) [G]
     float2 qf[G][C::QE / 2];      // scaled query rows, pairs of consecutive dims
@@ -581,6 +661,10 @@ struct CorePolicy {
 #pragma unroll
         for (int h = 0; h < G; ++h) o[h][0] = o[h][1] = make_float2(0.f, 0.f);
     }
+    // head0: the KV head's first query head
+    __device__ __forceinline__ void set_mods(const Params& p, int head0, int lane) {
+        mods.set(p, [&](int) { return head0 + (((lane % C::TPT) >> C::HSHIFT) & (G - 1)); });
+    }
 
     __device__ __forceinline__ void block(const unsigned char* Ks, const unsigned char* Vs,
                                           const float*, int n_valid, int bs_rt, float, int lane) {
@@ -597,7 +681,7 @@ struct CorePolicy {
             float2 acc2[G];
 #pragma unroll
             for (int h = 0; h < G; ++h) acc2[h] = make_float2(0.f, 0.f);
-            if (t < n_valid) {
+            if (t < n_valid && mods.sees(t)) {
 #pragma unroll
                 for (int i = 0; i < C::NCH; ++i) {
                     const uint4 raw = *reinterpret_cast<const uint4*>(
@@ -615,7 +699,9 @@ struct CorePolicy {
 #pragma unroll
             for (int h = 0; h < G; ++h) acc[h] = acc2[h].x + acc2[h].y;
             TReduce<G, C::TPT / 2>::run(acc, lane);
-            if (leader && t < bs) pb[t * G + hsel].x = (t < n_valid) ? acc[0] : -CUDART_INF_F;
+            if (leader && t < bs)
+                pb[t * G + hsel].x =
+                    (t < n_valid && mods.sees(t)) ? mods.apply(acc[0], t, 0) : -CUDART_INF_F;
         }
         __syncwarp();
         // -- online softmax, per head ---------------------------------------
@@ -652,7 +738,7 @@ struct CorePolicy {
 #pragma unroll 4
         for (int tt = 0; tt < bs; tt += C::TPSV) {
             const int t = tt + tv;
-            if (t < n_valid) {
+            if (t < n_valid && mods.sees(t)) {
                 float2 vf[2];
                 Elt<T>::four2(Vs + (uint32_t)(t * D + dl * 4) * C::ELT, vf);
 #pragma unroll
@@ -733,7 +819,8 @@ struct CorePolicy {
 // that way); merge_store writes every value to its own dim.
 // kPair: the tile holds two 8-row blocks, block i at byte 2048 i, each as
 // [half][8 rows][128 bytes] (block size 8, two blocks per work unit).
-template <typename T, int D, int G, int BSC, bool kPermV = false, bool kPair = false>
+template <typename T, int D, int G, int BSC, bool kPermV = false, bool kPair = false,
+          bool MOD = false>
 struct TcPolicy {
     static_assert(sizeof(T) == 2, "tensor-core path takes 16-bit pools");
     static_assert(BSC % 16 == 0 && BSC > 0, "tensor-core path needs a block size of 16k");
@@ -746,6 +833,8 @@ struct TcPolicy {
     static constexpr int kMinBlocks = 3;
     static constexpr int kKvBytes = sizeof(T);
     static constexpr int kScaleBytes = 0;
+    static constexpr bool kBlockScales = false;
+    static constexpr bool kMod = MOD;
     static constexpr int kUnitBlocks = 1;  // pool blocks per work unit
     static constexpr int KS = D / 16;      // QK k-steps (16 dims each)
     static constexpr int MT = D / 16;      // PV m-tiles (16 dims each)
@@ -757,6 +846,7 @@ struct TcPolicy {
     // m-tile instead of two.  fold() adds the two halves.
     static constexpr bool kPairHL = G <= 4;
 
+    ScoreMods<MOD, 2> mods;                // heads 2 tig, 2 tig + 1
     uint32_t qb[KS][2];                    // Q^T fragments (raw 16-bit query)
     float oacc[MT][4];                     // O^T accumulators
     float m_run[2], l_run[2];              // heads 2 tig, 2 tig + 1
@@ -783,6 +873,13 @@ struct TcPolicy {
     __device__ static __forceinline__ int col_head(int n) {
         const int h = kPairHL ? (n & 3) : n;
         return h < G ? h : -1;
+    }
+
+    __device__ __forceinline__ void set_mods(const Params& p, int head0, int lane) {
+        mods.set(p, [&](int i) {
+            const int h = col_head(2 * (lane & 3) + i);
+            return h >= 0 ? head0 + h : -1;
+        });
     }
 
     __device__ __forceinline__ void begin(const T* qp, float, int lane) {
@@ -818,6 +915,18 @@ struct TcPolicy {
             fence_proxy_async();
             __syncwarp();
         }
+        if constexpr (MOD) {
+            if (mods.n_lo > 0) {                   // and the rows before the first visible one
+                unsigned char* V = const_cast<unsigned char*>(Vs);
+                for (int i = lane; i < min(mods.n_lo, BSC) * 8; i += 32)
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf)
+                        *reinterpret_cast<uint4*>(V + line(i >> 3, hf) + (i & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async();
+                __syncwarp();
+            }
+        }
         // -- S^T = K_blk Q^T, scaled to base 2, masked past the end ----------
         float s[TT][4];
 #pragma unroll
@@ -829,11 +938,12 @@ struct TcPolicy {
                 ldsm_x4(a, swz(kbase, tt * 16 + (mi & 1) * 8 + r8, ks * 2 + (mi >> 1)));
                 Mma<T>::run(acc, a, qb[ks][0], qb[ks][1]);
             }
-            const bool v0 = tt * 16 + gid < n_valid, v1 = tt * 16 + gid + 8 < n_valid;
-            s[tt][0] = v0 ? acc[0] * qscale : -CUDART_INF_F;
-            s[tt][1] = v0 ? acc[1] * qscale : -CUDART_INF_F;
-            s[tt][2] = v1 ? acc[2] * qscale : -CUDART_INF_F;
-            s[tt][3] = v1 ? acc[3] * qscale : -CUDART_INF_F;
+            const int ra = tt * 16 + gid, rb = ra + 8;
+            const bool v0 = ra < n_valid && mods.sees(ra), v1 = rb < n_valid && mods.sees(rb);
+            s[tt][0] = v0 ? mods.apply(acc[0] * qscale, ra, 0) : -CUDART_INF_F;
+            s[tt][1] = v0 ? mods.apply(acc[1] * qscale, ra, 1) : -CUDART_INF_F;
+            s[tt][2] = v1 ? mods.apply(acc[2] * qscale, rb, 0) : -CUDART_INF_F;
+            s[tt][3] = v1 ? mods.apply(acc[3] * qscale, rb, 1) : -CUDART_INF_F;
         }
         // -- online softmax for heads 2 tig (j = 0) and 2 tig + 1 (j = 1) -----
         float mloc[2];
@@ -997,11 +1107,11 @@ struct TcPolicy {
 // 8 i .. 8 i + 7, the 2 KB at byte 2048 i: its first 64-dim half, then its
 // second, the same 128-byte swizzle pattern), and attended exactly like a
 // 16-token block.
-template <typename T, int D, int G>
-struct TcPolicy8x2 : TcPolicy<T, D, G, 16, false, true> {
+template <typename T, int D, int G, bool MOD = false>
+struct TcPolicy8x2 : TcPolicy<T, D, G, 16, false, true, MOD> {
     static constexpr int kUnitBlocks = 2;
     __device__ __forceinline__ TcPolicy8x2(float2* a, float2* b)
-        : TcPolicy<T, D, G, 16, false, true>(a, b) {}
+        : TcPolicy<T, D, G, 16, false, true, MOD>(a, b) {}
 };
 
 // ---------------------------------------------------- 8-bit pools on MMA --
@@ -1031,6 +1141,18 @@ struct TcPolicy8x2 : TcPolicy<T, D, G, 16, false, true> {
 constexpr int kFmtE4M3 = 0;
 constexpr int kFmtInt8 = 1;
 
+// Where an 8-bit pool's scales are.  kScBlock: one per (block, KV head), E4M3
+// or INT8 codes.  A tile of 16 rows lies inside one block, so its K scale is
+// one factor of the tile's scores and its V scale one factor of its weights;
+// the weights carry V scale / R like INT8's token scales (R the largest one
+// met).  The two 4-byte scales of a block come by cp.async beside the tile's
+// TMA copies and count as one more arrival on the stage's barrier: a block's
+// scales are 4 bytes at any 4-byte boundary, which no bulk copy can fetch.
+constexpr int kScPool = 0;
+constexpr int kScToken = 1;
+constexpr int kScBlock = 2;
+constexpr int kStageScales = 16;     // bytes per ring stage: two K, then two V scales
+
 // Four codes (bytes 0..3 of w) -> f16x2 of bytes (0, 1) and of bytes (2, 3).
 template <int FMT>
 __device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -1056,9 +1178,13 @@ __device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     }
 }
 
-template <typename T, int D, int G, int FMT>
-struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
-    using Base = TcPolicy<T, D, G, 16, true>;
+template <typename T, int D, int G, int FMT, int SC = FMT == kFmtInt8 ? kScToken : kScPool,
+          bool MOD = false, int UB = 1>
+struct Tc8Policy : TcPolicy<T, D, G, 16, true, false, MOD> {
+    using Base = TcPolicy<T, D, G, 16, true, false, MOD>;
+    static_assert(SC == kScBlock || SC == (FMT == kFmtInt8 ? kScToken : kScPool), "scale kind");
+    // the weights carry a V scale that varies within a piece
+    static constexpr bool kVaryV = SC != kScPool;
     static_assert(D == 128, "one 128-byte code row per token");
     static constexpr int KS = Base::KS;
     static constexpr int MT = Base::MT;
@@ -1069,7 +1195,8 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
     // thread cost no occupancy (the two-tile step needs about 160).
     static constexpr int kMinBlocks = 3;
     static constexpr int kKvBytes = 1;
-    static constexpr int kScaleBytes = FMT == kFmtInt8 ? 4 : 0;
+    static constexpr int kScaleBytes = SC == kScToken ? 4 : 0;
+    static constexpr bool kBlockScales = SC == kScBlock;
 
     float qs;             // scale * log2(e) * 2^-e (* the FP8 K scale)
     float vq;             // FP8: the V scale; INT8: 1
@@ -1080,8 +1207,8 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
     __device__ __forceinline__ Tc8Policy(float2* a, float2* b) : Base(a, b) {}
 
     __device__ __forceinline__ void setup(const Params& p) {
-        kq = FMT == kFmtE4M3 ? p.fp8_k_scale : 1.f;
-        vq = FMT == kFmtE4M3 ? p.fp8_v_scale : 1.f;
+        kq = SC == kScPool ? p.fp8_k_scale : 1.f;
+        vq = SC == kScPool ? p.fp8_v_scale : 1.f;
     }
 
     // 16-byte chunk c of row r of a 128-byte-swizzled tile (1 KB-aligned base)
@@ -1128,7 +1255,7 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
         this->l_run[0] = this->l_run[1] = 0.f;
         // INT8: R is the largest V scale met so far in the piece (raised, with
         // a rescale, when a tile brings a larger one); FP8: the pool's V scale
-        R = FMT == kFmtInt8 ? 0.f : vq;
+        R = kVaryV ? 0.f : vq;
         Rinv = 0.f;
     }
 
@@ -1174,27 +1301,37 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int ta = t0 + 16 * x + gid, tb = ta + 8;
-                const bool v0 = ta < n_valid, v1 = tb < n_valid;
+                const bool v0 = ta < n_valid && this->mods.sees(ta);
+                const bool v1 = tb < n_valid && this->mods.sees(tb);
                 float fa = qs, fb = qs;
                 sv[x][0] = sv[x][1] = 0.f;
-                if constexpr (FMT == kFmtInt8) {
+                if constexpr (SC == kScBlock) {
+                    // sc: the unit's K scales (first, second block), then its V scales
+                    const int k = UB == 2 ? x : 0;
+                    fa *= sc[k];
+                    fb = fa;
+                    if (t0 + 16 * x < n_valid) sv[x][0] = sv[x][1] = sc[2 + k];
+                    smax = fmaxf(smax, sv[x][0]);
+                }
+                if constexpr (SC == kScToken) {
                     fa *= v0 ? sc[ta] : 0.f;
                     fb *= v1 ? sc[tb] : 0.f;
                     sv[x][0] = v0 ? sc[bs + ta] : 0.f;
                     sv[x][1] = v1 ? sc[bs + tb] : 0.f;
                     smax = fmaxf(smax, fmaxf(sv[x][0], sv[x][1]));
                 }
-                s[x][0] = v0 ? (acc[x][0][0] + acc[x][1][0]) * fa : -CUDART_INF_F;
-                s[x][1] = v0 ? (acc[x][0][1] + acc[x][1][1]) * fa : -CUDART_INF_F;
-                s[x][2] = v1 ? (acc[x][0][2] + acc[x][1][2]) * fb : -CUDART_INF_F;
-                s[x][3] = v1 ? (acc[x][0][3] + acc[x][1][3]) * fb : -CUDART_INF_F;
+                const auto& md = this->mods;
+                s[x][0] = v0 ? md.apply((acc[x][0][0] + acc[x][1][0]) * fa, ta, 0) : -CUDART_INF_F;
+                s[x][1] = v0 ? md.apply((acc[x][0][1] + acc[x][1][1]) * fa, ta, 1) : -CUDART_INF_F;
+                s[x][2] = v1 ? md.apply((acc[x][0][2] + acc[x][1][2]) * fb, tb, 0) : -CUDART_INF_F;
+                s[x][3] = v1 ? md.apply((acc[x][0][3] + acc[x][1][3]) * fb, tb, 1) : -CUDART_INF_F;
             }
             // -- online softmax, heads 2 tig (j = 0) and 2 tig + 1 (j = 1); INT8:
             // the running largest V scale R moves with the maxima ----------------
             const float mloc[2] = {fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])),
                                    fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]))};
             if (__any_sync(FULL, mloc[0] > this->m_run[0] || mloc[1] > this->m_run[1] ||
-                                     (FMT == kFmtInt8 && smax > R))) {
+                                     (kVaryV && smax > R))) {
                 float alpha[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -1208,10 +1345,13 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
                     this->l_run[j] *= alpha[j];
                 }
                 float rf = 1.f;
-                if constexpr (FMT == kFmtInt8) {
+                if constexpr (kVaryV) {
                     float mx = smax;
+                    if constexpr (SC == kScToken) {
 #pragma unroll
-                    for (int off = 16; off >= 4; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+                        for (int off = 16; off >= 4; off >>= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+                    }
                     if (mx > R) {                     // (uniform: every lane sees all token rows)
                         Rinv = __frcp_rn(mx);
                         rf = R * Rinv;
@@ -1224,7 +1364,7 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 // V scales: P' = P * vscale_t / R
-                if constexpr (FMT == kFmtInt8) {
+                if constexpr (kVaryV) {
                     const float wa = sv[x][0] * Rinv, wb = sv[x][1] * Rinv;
                     s[x][0] *= wa; s[x][1] *= wa; s[x][2] *= wb; s[x][3] *= wb;
                 }
@@ -1240,7 +1380,7 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
                 for (int i = 0; i < 4; ++i) {
                     const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (tv + r < n_valid) v = chunk(Vt, r, gid);
+                    if (tv + r < n_valid && this->mods.sees(tv + r)) v = chunk(Vt, r, gid);
                     vw[i][0] = v.x; vw[i][1] = v.y; vw[i][2] = v.z; vw[i][3] = v.w;
                 }
 #pragma unroll
@@ -1272,10 +1412,12 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true> {
 
 // Two consecutive 16-row blocks per work unit (the kernel puts the second
 // block's code rows, and its INT8 scales, right after the first's).
-template <typename T, int D, int G, int FMT>
-struct Tc8Policy2 : Tc8Policy<T, D, G, FMT> {
+template <typename T, int D, int G, int FMT, int SC = FMT == kFmtInt8 ? kScToken : kScPool,
+          bool MOD = false>
+struct Tc8Policy2 : Tc8Policy<T, D, G, FMT, SC, MOD, 2> {
     static constexpr int kUnitBlocks = 2;
-    __device__ __forceinline__ Tc8Policy2(float2* a, float2* b) : Tc8Policy<T, D, G, FMT>(a, b) {}
+    __device__ __forceinline__ Tc8Policy2(float2* a, float2* b)
+        : Tc8Policy<T, D, G, FMT, SC, MOD, 2>(a, b) {}
 };
 
 // ---------------------------------------------- cross-range partial merge --
@@ -1287,7 +1429,8 @@ struct Tc8Policy2 : Tc8Policy<T, D, G, FMT> {
 // zero -- so the workspace needs no clearing: a stale counter of an earlier
 // call has that call's tag, and leftover data holds the call's tag only with
 // probability 2^-64.  Counting is a 128-bit compare-and-swap; the worker
-// whose count completes the set merges.
+// whose count completes the set merges, and leaves the counter at zero: a
+// captured graph's replays all carry the tag of their capture.
 __device__ __forceinline__ void cas128(unsigned long long* p, unsigned long long& lo,
                                        unsigned long long& hi, unsigned long long nlo,
                                        unsigned long long nhi) {
@@ -1304,8 +1447,9 @@ __device__ __forceinline__ bool count_piece(unsigned long long* ctr, unsigned lo
     while (true) {
         const unsigned long long elo = lo, ehi = hi;
         const unsigned long long next = (lo == tag ? hi : 0ull) + 1ull;
-        cas128(ctr, lo, hi, tag, next);            // lo, hi: the value found
-        if (lo == elo && hi == ehi) return next == (unsigned long long)pieces;
+        const bool last = next == (unsigned long long)pieces;
+        cas128(ctr, lo, hi, tag, last ? 0ull : next);   // lo, hi: the value found
+        if (lo == elo && hi == ehi) return last;
     }
 }
 
@@ -1524,6 +1668,15 @@ __device__ __forceinline__ int group_skip(const int* vg, int K, int n, int b) {
 // units of bsu tokens) less, for cascade decode, the leading units the
 // shared-prefix pass attended (skip_s[b]).  prefix[B] is the total.  Every
 // thread of the CTA calls; `report` flags contexts longer than the table.
+//
+// MOD (scored decode): the skipped leading units are the whole units before
+// the first visible position (a sequence that sees nothing has no unit).
+__device__ __forceinline__ int first_visible(const Params& p, int b, int L) {
+    int lo = p.window > 0 ? max(L - p.window, 0) : 0;
+    if (p.first != nullptr) lo = max(lo, p.first[b]);
+    return min(lo, L);
+}
+template <bool MOD = false>
 __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem, const Layout& lay,
                                             int bsu, bool cascade, bool report) {
     const int B = p.batch, tid = threadIdx.x, nthreads = blockDim.x;
@@ -1545,8 +1698,12 @@ __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem
         const int L = p.seq_lens[b];
         over |= L > cap;
         const int nb = (min(max(L, 0), cap) + bsu - 1) / bsu;
-        const int skip = cascade ? min(group_skip(vg, p.num_groups, nvg, b), nb) : 0;
-        if (cascade) skip_s[b] = skip;
+        int skip = cascade ? min(group_skip(vg, p.num_groups, nvg, b), nb) : 0;
+        if constexpr (MOD) {
+            const int Lc = min(max(L, 0), cap), lo = first_visible(p, b, Lc);
+            skip = lo == Lc ? nb : lo / bsu;
+        }
+        if (cascade || MOD) skip_s[b] = skip;
         local += nb - skip;
     }
     if (over && report) atomicOr(p.err, KV_DEVERR_SEQ_RANGE);
@@ -1555,7 +1712,7 @@ __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem
     for (int b = b0; b < b1; ++b) {
         prefix[b] = run;
         const int nb = (min(max(p.seq_lens[b], 0), cap) + bsu - 1) / bsu;
-        run += nb - (cascade ? skip_s[b] : 0);
+        run += nb - (cascade || MOD ? skip_s[b] : 0);
     }
     if (tid == 0) prefix[B] = total;
 }
@@ -1571,7 +1728,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
     const int B = p.batch, S = p.stages, H = p.num_kv_heads, bs = p.bs;
     constexpr int UB = Pol::kUnitBlocks;           // pool blocks per work unit
     const int bsu = bs * UB;                       // tokens per work unit
-    const Layout lay(S, B, bsu, G, D, ELT, p.num_groups, Pol::kScaleBytes);
+    constexpr bool MOD = Pol::kMod;
+    const Layout lay(S, B, bsu, G, D, ELT, MOD ? 0 : p.num_groups, Pol::kScaleBytes,
+                     Pol::kBlockScales ? kStageScales : 0, MOD);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.full);
     volatile int* valid = reinterpret_cast<volatile int*>(smem + lay.valid);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + lay.misc);
@@ -1583,11 +1742,15 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
     const int cap = p.max_blocks * bs;              // longest context a table can hold
     // cascade: the groups' shared prefix is counted in whole units of UB
     // blocks (load_groups), so paired-block units skip it like single ones
-    const bool cascade = p.num_groups > 0;
+    // (scored decode: whole units before the first visible position, skipped
+    // through the same counts)
+    const bool cascade = !MOD && p.num_groups > 0;
+    const bool skips = MOD || cascade;
 
     // -- 1. the blocks-per-sequence prefix of the clamped lengths -----------
     if (tid == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full[s]), 1);
+        // (block scales: their cp.async copies are an arrival of their own)
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full[s]), Pol::kBlockScales ? 2 : 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1599,7 +1762,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
     // reads the prefix states (and, at the latest, before each warp exits,
     // so that this grid never ends before the prefix pass).
     if (!cascade) pdl_wait();
-    unit_prefix(p, smem, lay, bsu, cascade, blockIdx.x == 0);
+    unit_prefix<MOD>(p, smem, lay, bsu, cascade, blockIdx.x == 0);
     __syncthreads();
     // sequences no unit covers: zeros, or (cascade) the prefix state alone
     for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -1660,7 +1823,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
             const int nb = prefix[b + 1] - prefix[b];
             const int r = uu - prefix[b] * H;
             gg = r / nb;
-            const int lb = ((cascade ? skip_s[b] : 0) + (r - gg * nb)) * UB;
+            const int lb = ((skips ? skip_s[b] : 0) + (r - gg * nb)) * UB;
             const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
             id = __ldg(row + lb);
             if (UB == 2 && (lb + 1) * bs < min(max(p.seq_lens[b], 0), cap))
@@ -1743,10 +1906,23 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
                                   (uint32_t)bs * 4u, fb);
                     }
                 }
+                if constexpr (Pol::kBlockScales) {
+                    float* sdst = reinterpret_cast<float*>(smem + lay.sring + st * kStageScales);
+                    const size_t si = (size_t)id * H + gg;
+                    cp_async4(sdst, p.k_scales + si);
+                    cp_async4(sdst + 2, p.v_scales + si);
+                    if (second) {
+                        const size_t si2 = (size_t)id2 * H + gg;
+                        cp_async4(sdst + 1, p.k_scales + si2);
+                        cp_async4(sdst + 3, p.v_scales + si2);
+                    }
+                    cp_async_arrive(fb);
+                }
             } else {
                 valid[st] = 0;
                 atomicOr(p.err, KV_DEVERR_BLOCK_RANGE);
                 mbar_arrive(fb);
+                if (Pol::kBlockScales) mbar_arrive(fb);
             }
         }
     };
@@ -1763,11 +1939,12 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
         const int seg_start = prefix[b] * H + g * nb;
         const int piece_end = min(end, seg_start + nb);
         const int Lb = min(max(p.seq_lens[b], 0), cap);
-        const int skip = cascade ? skip_s[b] : 0;
+        const int skip = skips ? skip_s[b] : 0;
+        const int lo = MOD ? first_visible(p, b, Lb) : 0;
         const size_t head0 = (size_t)b * p.num_q_heads + (size_t)g * G;
         // cascade: stage this (b, g)'s prefix state in shared memory while
         // the piece's blocks are attended
-        if (skip > 0) {
+        if (cascade && skip > 0) {
             pdl_wait();                            // the prefix pass's states are written
             __syncwarp();                          // the last piece's reads are done
             for (int i = lane; i < G * D / 4; i += 32)
@@ -1776,6 +1953,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
         }
 
         pol.begin(qbase + head0 * D, p.qscale, lane);
+        if constexpr (MOD) pol.set_mods(p, g * G, lane);
 
         for (int uu = u; uu < piece_end; ++uu) {
             const int s = cs;
@@ -1795,9 +1973,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
             if (ok && valid[s]) {
                 const int j = skip + j0 + (uu - u);
                 const unsigned char* Ks = ring + (size_t)s * lay.stage_bytes;
-                const float* sc = Pol::kScaleBytes > 0
-                                      ? reinterpret_cast<const float*>(smem + lay.sring) + s * 2 * bsu
-                                      : nullptr;
+                const float* sc =
+                    Pol::kScaleBytes > 0
+                        ? reinterpret_cast<const float*>(smem + lay.sring) + s * 2 * bsu
+                        : (Pol::kBlockScales
+                               ? reinterpret_cast<const float*>(smem + lay.sring + s * kStageScales)
+                               : nullptr);
+                if constexpr (MOD) pol.mods.unit(lo - j * bsu, j * bsu - (Lb - 1));
                 pol.block(Ks, Ks + bsu * D * ELT, sc, min(bsu, Lb - j * bsu), bsu, p.qscale, lane);
             }
             __syncwarp();                          // every lane is done with stage s
@@ -1813,9 +1995,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
             po.out = obase + head0 * D;
             po.part_o = p.part_o + ps * G * D;
             po.part_lse = p.part_lse + ps * G;
-            po.pst_o = skip > 0 ? pst_s : nullptr;
-            po.pst_lse = skip > 0 ? pst_s + G * D : nullptr;
-            if (skip > 0) {
+            po.pst_o = cascade && skip > 0 ? pst_s : nullptr;
+            po.pst_lse = cascade && skip > 0 ? pst_s + G * D : nullptr;
+            if (cascade && skip > 0) {
                 cp_async_wait_all();
                 __syncwarp();
             }
@@ -1912,7 +2094,7 @@ __device__ __forceinline__ void lse_range(const float* part_o, const float* part
 // shared memory (long contexts: dozens of partials per pair); merge_wpp = 1:
 // a warp per pair.  The split kernel's cut is recomputed here from the same
 // seq_lens and grid.
-template <typename T, int D, int G, int UB>
+template <typename T, int D, int G, int UB, bool MOD = false>
 __global__ void __launch_bounds__(SPLIT_THREADS) paged_decode_merge(const Params p) {
     constexpr int EPL = merge_epl<G, D>();
     constexpr int NP = G * D / (32 * EPL);         // element passes of a warp
@@ -1920,13 +2102,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS) paged_decode_merge(const Params
     unsigned char* smem = smem_align_1k(smem_raw);
     const int B = p.batch, H = p.num_kv_heads;
     const int bsu = p.bs * UB;
-    const Layout lay(0, B, bsu, G, D, 2, p.num_groups, 0);
+    const Layout lay(0, B, bsu, G, D, 2, MOD ? 0 : p.num_groups, 0, 0, MOD);
     const int* prefix = reinterpret_cast<const int*>(smem + lay.prefix);
     const int* skip_s = reinterpret_cast<const int*>(smem + lay.skip);
     float* red = reinterpret_cast<float*>(smem + lay.pst);   // [NCW][NP][32][EPL + 2]
-    const bool cascade = p.num_groups > 0;
+    const bool cascade = !MOD && p.num_groups > 0;
     pdl_wait();                                    // the split kernel's partials are visible
-    unit_prefix(p, smem, lay, bsu, cascade, false);
+    unit_prefix<MOD>(p, smem, lay, bsu, cascade, false);
     __syncthreads();
     const WorkCut cut(prefix, B, H, p.num_ctas * NCW);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -2049,6 +2231,11 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     p.v_scales = pool.v_scales;
     p.fp8_k_scale = pool.fp8_k_scale;
     p.fp8_v_scale = pool.fp8_v_scale;
+    p.softcap = call.mods ? call.mods->softcap : 0.f;
+    p.inv_softcap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
+    p.slopes = call.mods ? call.mods->alibi_slopes : nullptr;
+    p.window = call.mods ? call.mods->window : 0;
+    p.first = call.mods ? call.mods->first_visible : nullptr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.num_ctas);
     cfg.blockDim = dim3(SPLIT_THREADS);
@@ -2070,8 +2257,9 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
         e = cudaLaunchKernelEx(&cfg, split, pool.tmap_k, pool.tmap_v, p);
     if (e != cudaSuccess || p.merge_wpp == 0) return e;
     // the partials of (b, g) cut across warps, merged behind the split kernel
-    auto merge = paged_decode_merge<T, D, G, Pol::kUnitBlocks>;
-    const Layout ml(0, call.batch, pool.block_size * Pol::kUnitBlocks, G, D, 2, call.num_groups, 0);
+    auto merge = paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod>;
+    const Layout ml(0, call.batch, pool.block_size * Pol::kUnitBlocks, G, D, 2, call.num_groups, 0, 0,
+                    Pol::kMod);
     const size_t merge_smem = ml.pst + merge_red_bytes<G, D>() + 1024;
     cfg.gridDim = dim3((unsigned)std::max(1, std::min((pairs * p.merge_wpp + NCW - 1) / NCW,
                                                       pool.num_sms * 4)));
@@ -2109,8 +2297,21 @@ inline bool use_tensor_cores(const kv_pool& pool, int G) {
            pool.has_h2_maps;
 }
 
-template <typename T, int D, int G, template <typename, int, int, class> class Fn, typename... A>
+template <typename T, int D, int G, bool MOD, template <typename, int, int, class> class Fn,
+          typename... A>
 cudaError_t with_policy(int bs, bool tc, A... args) {
+    if constexpr (MOD) {
+        // (scored decode: the same tensor-core tiles; one CUDA-core instance
+        // for every other block size)
+        if constexpr (kTensorCores<T, D, G>) {
+            if (tc && bs == 8) return Fn<T, D, G, TcPolicy8x2<T, D, G, true>>::run(args...);
+            if (tc && bs == 16)
+                return Fn<T, D, G, TcPolicy<T, D, G, 16, false, false, true>>::run(args...);
+            if (tc && bs == 32)
+                return Fn<T, D, G, TcPolicy<T, D, G, 32, false, false, true>>::run(args...);
+        }
+        return Fn<T, D, G, CorePolicy<T, D, G, 0, true>>::run(args...);
+    } else {
     if constexpr (kTensorCores<T, D, G>) {
         if (tc && bs == 8) return Fn<T, D, G, TcPolicy8x2<T, D, G>>::run(args...);
         if (tc && bs == 16) return Fn<T, D, G, TcPolicy<T, D, G, 16>>::run(args...);
@@ -2122,6 +2323,7 @@ cudaError_t with_policy(int bs, bool tc, A... args) {
         if (bs == 32) return Fn<T, D, G, CorePolicy<T, D, G, 32>>::run(args...);
     }
     return Fn<T, D, G, CorePolicy<T, D, G, 0>>::run(args...);
+    }
 }
 
 template <typename T, int D, int G, class Pol> struct LaunchFn {
@@ -2136,13 +2338,13 @@ template <typename T, int D, int G, class Pol> struct AttrsFn {
     }
 };
 
-template <typename T>
+template <typename T, bool MOD = false>
 cudaError_t dispatch(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
                      cudaStream_t stream) {
     const bool tc = use_tensor_cores(pool, plan.group);
 #define PKV_CASE(DD, GG)                                                                 \
     if (pool.head_dim == DD && plan.group == GG)                                         \
-        return with_policy<T, DD, GG, LaunchFn>(pool.block_size, tc, &pool, &call, &plan, \
+        return with_policy<T, DD, GG, MOD, LaunchFn>(pool.block_size, tc, &pool, &call, &plan, \
                                                 stream);
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)
     PKV_CASE(128, 1) PKV_CASE(128, 2) PKV_CASE(128, 4) PKV_CASE(128, 8)
@@ -2150,12 +2352,12 @@ cudaError_t dispatch(const kv_pool& pool, const DecodeCall& call, const DecodePl
     return cudaErrorNotSupported;
 }
 
-template <typename T>
+template <typename T, bool MOD = false>
 cudaError_t attrs(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm) {
     const bool tc = use_tensor_cores(pool, group);
 #define PKV_CASE(DD, GG)                                                                        \
     if (pool.head_dim == DD && group == GG)                                                     \
-        return with_policy<T, DD, GG, AttrsFn>(pool.block_size, tc, smem, ctas_per_sm);
+        return with_policy<T, DD, GG, MOD, AttrsFn>(pool.block_size, tc, smem, ctas_per_sm);
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)
     PKV_CASE(128, 1) PKV_CASE(128, 2) PKV_CASE(128, 4) PKV_CASE(128, 8)
 #undef PKV_CASE
@@ -2175,40 +2377,42 @@ inline bool q8_pairs_blocks(const kv_pool& pool, int G) {
     return pool.block_size == 16 && (G == 1 || G == 2 || G == 4 || G == 8);
 }
 
-template <typename T, int FMT, template <typename, int, int, class> class Fn, typename... A>
+template <typename T, int FMT, int SC, bool MOD, template <typename, int, int, class> class Fn,
+          typename... A>
 cudaError_t with_q8_policy(int G, bool pairs, A... args) {
-    if (pairs && G == 1) return Fn<T, 128, 1, Tc8Policy2<T, 128, 1, FMT>>::run(args...);
-    if (pairs && G == 2) return Fn<T, 128, 2, Tc8Policy2<T, 128, 2, FMT>>::run(args...);
-    if (pairs && G == 4) return Fn<T, 128, 4, Tc8Policy2<T, 128, 4, FMT>>::run(args...);
-    if (pairs && G == 8) return Fn<T, 128, 8, Tc8Policy2<T, 128, 8, FMT>>::run(args...);
-    if (G == 1) return Fn<T, 128, 1, Tc8Policy<T, 128, 1, FMT>>::run(args...);
-    if (G == 2) return Fn<T, 128, 2, Tc8Policy<T, 128, 2, FMT>>::run(args...);
-    if (G == 4) return Fn<T, 128, 4, Tc8Policy<T, 128, 4, FMT>>::run(args...);
-    if (G == 8) return Fn<T, 128, 8, Tc8Policy<T, 128, 8, FMT>>::run(args...);
+#define PKV_CASE(GG)                                                                             \
+    if (G == GG)                                                                                 \
+        return pairs ? Fn<T, 128, GG, Tc8Policy2<T, 128, GG, FMT, SC, MOD>>::run(args...)        \
+                     : Fn<T, 128, GG, Tc8Policy<T, 128, GG, FMT, SC, MOD>>::run(args...);
+    PKV_CASE(1) PKV_CASE(2) PKV_CASE(4) PKV_CASE(8)
+#undef PKV_CASE
     return cudaErrorNotSupported;
 }
 
-template <typename T>
+// One scale kind per translation unit (SC; kScPool and kScToken together, as
+// kScPlain): the pools of another kind are not this unit's.
+constexpr int kScPlain = -1;
+template <typename T, int SC, bool MOD, template <typename, int, int, class> class Fn, typename... A>
+cudaError_t by_format(const kv_pool& pool, int group, A... args) {
+    if (!q8_shape_ok(pool) || pool.block_scales != (SC == kScBlock)) return cudaErrorNotSupported;
+    const bool pairs = q8_pairs_blocks(pool, group);
+    constexpr int kF = SC == kScBlock ? kScBlock : kScPool, kI = SC == kScBlock ? kScBlock : kScToken;
+    if (pool.cache_dtype == KV_FP8_E4M3)
+        return with_q8_policy<T, kFmtE4M3, kF, MOD, Fn>(group, pairs, args...);
+    if (pool.cache_dtype == KV_INT8)
+        return with_q8_policy<T, kFmtInt8, kI, MOD, Fn>(group, pairs, args...);
+    return cudaErrorNotSupported;
+}
+
+template <typename T, int SC = kScPlain, bool MOD = false>
 cudaError_t dispatch_q8(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
                         cudaStream_t stream) {
-    if (!q8_shape_ok(pool)) return cudaErrorNotSupported;
-    const bool pairs = q8_pairs_blocks(pool, plan.group);
-    if (pool.cache_dtype == KV_FP8_E4M3)
-        return with_q8_policy<T, kFmtE4M3, LaunchFn>(plan.group, pairs, &pool, &call, &plan, stream);
-    if (pool.cache_dtype == KV_INT8)
-        return with_q8_policy<T, kFmtInt8, LaunchFn>(plan.group, pairs, &pool, &call, &plan, stream);
-    return cudaErrorNotSupported;
+    return by_format<T, SC, MOD, LaunchFn>(pool, plan.group, &pool, &call, &plan, stream);
 }
 
-template <typename T>
+template <typename T, int SC = kScPlain, bool MOD = false>
 cudaError_t attrs_q8(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm) {
-    if (!q8_shape_ok(pool)) return cudaErrorNotSupported;
-    const bool pairs = q8_pairs_blocks(pool, group);
-    if (pool.cache_dtype == KV_FP8_E4M3)
-        return with_q8_policy<T, kFmtE4M3, AttrsFn>(group, pairs, smem, ctas_per_sm);
-    if (pool.cache_dtype == KV_INT8)
-        return with_q8_policy<T, kFmtInt8, AttrsFn>(group, pairs, smem, ctas_per_sm);
-    return cudaErrorNotSupported;
+    return by_format<T, SC, MOD, AttrsFn>(pool, group, smem, ctas_per_sm);
 }
 
 }  // namespace dec

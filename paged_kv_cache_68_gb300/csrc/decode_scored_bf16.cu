@@ -1,0 +1,15 @@
+// Scored decode kernels (capped, biased, masked) for bf16 pools.
+#include "decode_kernel.cuh"
+
+namespace pagedkv {
+
+cudaError_t decode_dispatch_scored_bf16(const kv_pool& pool, const DecodeCall& call,
+                                   const DecodePlan& plan, cudaStream_t stream) {
+    return dec::dispatch<__nv_bfloat16, true>(pool, call, plan, stream);
+}
+
+cudaError_t decode_attrs_scored_bf16(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm) {
+    return dec::attrs<__nv_bfloat16, true>(pool, group, smem, ctas_per_sm);
+}
+
+}  // namespace pagedkv

@@ -1,0 +1,15 @@
+// Scored decode kernels for 8-bit pools with pool or token scales, f16 queries.
+#include "decode_kernel.cuh"
+
+namespace pagedkv {
+
+cudaError_t decode_dispatch_scored_q8_f16(const kv_pool& pool, const DecodeCall& call,
+                                   const DecodePlan& plan, cudaStream_t stream) {
+    return dec::dispatch_q8<__half, dec::kScPlain, true>(pool, call, plan, stream);
+}
+
+cudaError_t decode_attrs_scored_q8_f16(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm) {
+    return dec::attrs_q8<__half, dec::kScPlain, true>(pool, group, smem, ctas_per_sm);
+}
+
+}  // namespace pagedkv

@@ -40,6 +40,12 @@ struct kv_pool {
     void* v;
     float* k_scales = nullptr;   // KV_INT8: [num_blocks][num_kv_heads][block_size]
     float* v_scales = nullptr;
+    bool block_scales = false;   // one scale per block and head: [num_blocks][num_kv_heads]
+    // block-scaled pools, kv_append of many rows: the row of this call that
+    // goes to each slot, and the last one that goes to each block (index + 1;
+    // 0 between calls)
+    int* d_owner = nullptr;      // [num_blocks * block_size]
+    int* d_leader = nullptr;     // [num_blocks]
     float fp8_k_scale = 1.f;     // KV_FP8_E4M3: per-pool scales
     float fp8_v_scale = 1.f;
     int* d_err;             // device error word (KV_DEVERR_* bits)
@@ -61,6 +67,7 @@ struct kv_pool {
     int plan_batch = -1;
     int plan_hq = -1;
     int plan_groups = -1;
+    bool plan_scored = false;
     pagedkv::DecodePlan plan;
 };
 
@@ -129,6 +136,7 @@ struct PrefillCall {
     int batch;
     int num_q_heads;
     float scale;
+    const kv_score_mods* mods = nullptr;   // scored prefill
 };
 cudaError_t launch_prefill(const kv_pool& pool, const PrefillCall& call, cudaStream_t stream);
 
@@ -154,6 +162,10 @@ kv_status decode_with_workspace(kv_pool* pool, const void* q, void* out,
 // process-wide counter through the splitmix64 finaliser, keyed once per
 // process from the clock and a random device.
 unsigned long long new_counter_tag();
+
+// kv_append on a block-scaled pool.
+cudaError_t launch_append_block_scaled(const kv_pool& pool, const void* k_new, const void* v_new,
+                                       const int64_t* slots, int num_tokens, cudaStream_t stream);
 
 cudaError_t launch_append(const kv_pool& pool, const void* k_new, const void* v_new,
                           const int64_t* slots, int num_tokens, cudaStream_t stream);
@@ -185,12 +197,13 @@ struct DecodeCall {
     int num_groups = 0;
     const float* pst_o = nullptr;
     const float* pst_lse = nullptr;
+    const kv_score_mods* mods = nullptr;   // scored decode
 };
 
 // Fill `plan` for this pool / batch / head count on the current device
 // (cached per pool).  Returns cudaErrorNotSupported for shapes with no
 // compiled kernel.
-cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups,
+cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups, bool scored,
                         DecodePlan* plan);
 
 cudaError_t launch_decode(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
@@ -208,6 +221,26 @@ cudaError_t decode_dispatch_q8_f16(const kv_pool&, const DecodeCall&, const Deco
 cudaError_t decode_dispatch_q8_bf16(const kv_pool&, const DecodeCall&, const DecodePlan&, cudaStream_t);
 cudaError_t decode_attrs_q8_f16(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm);
 cudaError_t decode_attrs_q8_bf16(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm);
+
+// block-scaled pools, and scored decode on any pool (kinds of kernel with a
+// translation unit per query type of their own)
+#define PKV_DECODE_UNIT(name)                                                                    \
+    cudaError_t decode_dispatch_##name(const kv_pool&, const DecodeCall&, const DecodePlan&,     \
+                                       cudaStream_t);                                            \
+    cudaError_t decode_attrs_##name(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm);
+PKV_DECODE_UNIT(block_f16) PKV_DECODE_UNIT(block_bf16)
+PKV_DECODE_UNIT(scored_f32) PKV_DECODE_UNIT(scored_f16) PKV_DECODE_UNIT(scored_bf16)
+PKV_DECODE_UNIT(scored_q8_f16) PKV_DECODE_UNIT(scored_q8_bf16)
+PKV_DECODE_UNIT(scored_block_f16) PKV_DECODE_UNIT(scored_block_bf16)
+#undef PKV_DECODE_UNIT
+
+// mods within their documented ranges
+inline bool mods_ok(const kv_score_mods* m) {
+    return m && m->softcap >= 0.f && m->softcap <= 3.4e38f && m->window >= 0 &&
+           !(reinterpret_cast<uintptr_t>(m->alibi_slopes) & 3u) &&
+           !(reinterpret_cast<uintptr_t>(m->first_visible) & 3u) &&
+           !(reinterpret_cast<uintptr_t>(m->prefix_lens) & 3u);
+}
 
 inline bool is_q8(const kv_pool& pool) {
     return pool.cache_dtype == KV_FP8_E4M3 || pool.cache_dtype == KV_INT8;

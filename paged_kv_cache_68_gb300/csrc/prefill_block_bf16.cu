@@ -1,0 +1,10 @@
+// Prefill kernels for block-scaled 8-bit pools, bf16 queries.
+#include "prefill_launch.cuh"
+
+namespace pagedkv {
+
+cudaError_t prefill_block_bf16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
+    return pf::launch_block<__nv_bfloat16, false>(pool, c, stream);
+}
+
+}  // namespace pagedkv

@@ -1,0 +1,10 @@
+// Prefill kernels for 16-bit pools and 8-bit pools with pool or token scales, f16 queries.
+#include "prefill_launch.cuh"
+
+namespace pagedkv {
+
+cudaError_t prefill_f16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
+    return pf::launch_format<__half, false>(pool, c, stream);
+}
+
+}  // namespace pagedkv

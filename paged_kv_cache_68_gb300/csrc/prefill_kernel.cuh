@@ -165,7 +165,25 @@ struct Params {
     const float* v_scales;
     int num_kv_heads;
     unsigned long long wait_ns;   // limit of one pipeline wait (the pool's setting)
+    // scored prefill (MOD): the cap (0: none) and its reciprocal, the heads'
+    // slopes (null: none), the window (0: none), each query's first visible
+    // position (null: 0) and each request's prefix (null: none)
+    float softcap, inv_softcap;
+    const float* slopes;          // [num_q_heads]
+    int window;
+    const int32_t* first;         // [num_tokens]
+    const int32_t* prefix;        // [batch]
 };
+
+// The positions lo..hi that a query at position pos of a request of length L
+// sees (none if lo > hi): causal or inside the prefix, in the window, in its
+// document.  `token`: the query's row in the flattened stream.
+__device__ __forceinline__ void visible_range(const Params& p, int pos, int L, int prefix,
+                                              int token, int& lo, int& hi) {
+    lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+    if (p.first != nullptr) lo = max(lo, p.first[token]);
+    hi = pos < 0 ? -1 : max(pos, min(prefix, L) - 1);
+}
 
 // ------------------------------------------------------------ tcgen05 PTX --
 __device__ __forceinline__ void tc_fence_before() {
@@ -362,14 +380,25 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
 }
 
 // FMT: -1 for 16-bit pools (of type T), else the 8-bit pool's code format
-// (T is then the queries' type); the K / V maps address code rows.
-template <typename T, int G, int FMT = -1>
+// (T is then the queries' type); the K / V maps address code rows.  SC: where
+// an 8-bit pool's scales are; a block's scale is read once for each of its
+// boxes and spread over the tile's tokens in the scale ring, so the softmax
+// reads block scales as it reads token scales.
+//
+// MOD (scored prefill): scores are capped, biased and masked between the QK
+// product and the softmax, in base 2 (see ScoreMods): a cap costs two MUFU
+// operations a score beside the softmax's one.  The tiles walked run from the
+// first to the last position that any of the CTA's queries sees; each row
+// masks what lies outside its own lo..hi.
+template <typename T, int G, int FMT = -1,
+          int SC = FMT == dec::kFmtInt8 ? dec::kScToken : dec::kScPool, bool MOD = false>
 __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     paged_prefill(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
     constexpr bool Q8 = FMT >= 0;
-    constexpr bool SCALES = FMT == dec::kFmtInt8;
+    constexpr bool SCALES = Q8 && SC != dec::kScPool;
+    constexpr bool BLOCKSC = Q8 && SC == dec::kScBlock;
     // 8-bit pools: the products run on f16 (bf16 queries are converted)
     using MT = typename std::conditional<Q8, __half, T>::type;
     constexpr bool QCONV = Q8 && !std::is_same<T, __half>::value;
@@ -443,7 +472,32 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     const int Pmax = P0 + (nstreams == 2 ? QT + nqb : nqa) - 1;   // the last query's (<= L - 1)
     // every active stream walks all tiles (rows past their own limit are
     // masked), so each K/V tile has exactly `nstreams` consumers
-    const int ntiles = Pmax >= 0 ? Pmax / BN + 1 : 0;
+    int ntiles = Pmax >= 0 ? Pmax / BN + 1 : 0;
+    int jt0 = 0;                                   // the first tile walked
+    int vbeg = 0, vend = L;                        // positions some query of the CTA sees
+    int prefix = 0;
+    if constexpr (MOD) {
+        prefix = p.prefix != nullptr ? p.prefix[b] : 0;
+        int* span = reinterpret_cast<int*>(smem + LY::order) + kMaxRanked + 1;   // lo, hi
+        if (tid == 0) {
+            span[0] = 0x7fffffff;
+            span[1] = -1;
+        }
+        __syncthreads();
+        if (tid < nqa + max(nqb, 0)) {
+            int lo, hi;
+            visible_range(p, P0 + tid, L, prefix, cu0 + q0 + tid, lo, hi);
+            if (lo <= hi) {
+                atomicMin(&span[0], lo);
+                atomicMax(&span[1], hi);
+            }
+        }
+        __syncthreads();
+        vbeg = span[0];
+        vend = span[1] + 1;
+        jt0 = vend > 0 ? vbeg / BN : 0;
+        ntiles = vend > 0 ? (vend - 1) / BN - jt0 + 1 : 0;
+    }
 
     // -- set-up: barriers, TMEM ----------------------------------------------
     if (tid == 0) {
@@ -509,7 +563,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 const float* gsc = is_k ? p.k_scales : p.v_scales;
                 int codes_issued = 0;
                 auto issue_codes = [&](int jj) {
-                    const int t = jj * BN + lane * R;   // first token of this lane's box
+                    const int t = (jt0 + jj) * BN + lane * R;   // first token of this lane's box
                     int row = -1, id = -1;
                     bool load = false;
                     if (lane < nbox && t < L) {
@@ -520,13 +574,16 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                     }
                     const unsigned mask = __ballot_sync(FULL, load);
                     const uint32_t cb = bar(cfull0 + jj % CST);
-                    const uint32_t per_box = (uint32_t)R * 128u + (SCALES ? (uint32_t)R * 4u : 0u);
+                    const uint32_t per_box = (uint32_t)R * 128u + (SCALES && !BLOCKSC ? (uint32_t)R * 4u : 0u);
                     if (lane == 0) dec::mbar_arrive_tx(cb, (uint32_t)__popc(mask) * per_box);
                     __syncwarp();
                     if (load) {
                         dec::tma_load_3d(code0 + (uint32_t)(jj % CST) * CTILE + (uint32_t)lane * R * 128u,
                                          map, 0, g, row, cb);
-                        if constexpr (SCALES) {
+                        if constexpr (BLOCKSC) {
+                            dec::cp_async4(csc + (jj % CST) * BN + lane,
+                                           gsc + (size_t)id * p.num_kv_heads + g);
+                        } else if constexpr (SCALES) {
                             const size_t srow = ((size_t)id * p.num_kv_heads + g) * bs + t % bs;
                             dec::bulk_load(dec::smem_u32(csc + (jj % CST) * BN + lane * R), gsc + srow,
                                            (uint32_t)R * 4u, cb);
@@ -606,8 +663,17 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                     if constexpr (SCALES) {
                         float* ring = reinterpret_cast<float*>(smem + LY::sc) + (j % SCS) * 2 * BN +
                                       (is_k ? 0 : BN);
-                        ring[lane] = csc[cs * BN + lane];
-                        ring[lane + 32] = csc[cs * BN + lane + 32];
+                        if constexpr (BLOCKSC) {
+                            // (one scale per box; this also waits for the next
+                            // tile's, issued a tile ago)
+                            dec::cp_async_wait_all();
+                            __syncwarp();
+                            ring[lane] = csc[cs * BN + lane / R];
+                            ring[lane + 32] = csc[cs * BN + (lane + 32) / R];
+                        } else {
+                            ring[lane] = csc[cs * BN + lane];
+                            ring[lane + 32] = csc[cs * BN + lane + 32];
+                        }
                     }
                     dec::fence_proxy_async();
                     __syncwarp();
@@ -627,6 +693,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                     }
                 }
                 // Drain: no copy may still be landing in shared memory at exit.
+                if (BLOCKSC) dec::cp_async_wait_all();
                 if (lane == 0) {
                     bool ok = !is_k || dec::mbar_wait(bar(BAR_Q), 0);
                     for (int jj = max(0, codes_issued - CST); jj < codes_issued; ++jj)
@@ -644,7 +711,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                         ok = wait_or_abort(bar(empty0 + slot), (j / nst - 1) & 1, abort_flag, p.err,
                                            p.wait_ns);
                     if (!__shfl_sync(FULL, ok ? 1 : 0, 0)) break;
-                    const int t = j * BN + lane * R;   // first token of this lane's box
+                    const int t = (jt0 + j) * BN + lane * R;   // first token of this lane's box
                     int row = -1;
                     bool load = false;
                     if (lane < nbox && t < L) {
@@ -782,7 +849,14 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
         const int qi = r / G, hh = r % G;
         const int nq = x == 0 ? nqa : nqb;
         const bool valid = qi < nq;
-        const int lim = valid ? P0 + x * QT + qi : -1;   // last visible position
+        const int pos = P0 + x * QT + qi;          // the query's position
+        int lim = valid ? pos : -1;                // last visible position
+        int lo = 0;                                // first visible position
+        float slope2 = 0.f;                        // the head's slope, base 2
+        if constexpr (MOD) {
+            if (valid) visible_range(p, pos, L, prefix, cu0 + q0 + x * QT + qi, lo, lim);
+            if (p.slopes != nullptr) slope2 = p.slopes[g * G + hh] * 1.4426950408889634f;
+        }
         const uint32_t trow = tmem + (uint32_t)x * COL_STREAM + ((uint32_t)(32 * qd) << 16);
         const int stid = tid - x * NSOFT * 32;     // thread index within the stream
         float qs = p.qscale;
@@ -802,8 +876,11 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 if (ok) qs *= reinterpret_cast<const float*>(smem + LY::qinv)[x * BM + r];
             }
         }
+        // (MOD scales the scores before it caps and biases them)
+        const float row_qs = qs;
+        if constexpr (MOD) qs = 1.f;
         for (int j = 0; ok && j < ntiles; ++j) {
-            const int t0 = j * BN;
+            const int t0 = (jt0 + j) * BN;
             uint32_t sv[2][32];
             ok = wait_warp(sbar(x, SB_SF), j & 1);
             if (!ok) break;
@@ -824,6 +901,50 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * tsc[32 * c + e]);
+            }
+            if constexpr (MOD) {
+                const float2 q2 = make_float2(row_qs, row_qs);
+                if (p.softcap > 0.f) {
+                    const float cap2 = p.softcap * 1.4426950408889634f;
+                    const float2 k2 = __fmul2_rn(q2, make_float2(2.f * p.inv_softcap, 2.f * p.inv_softcap));
+                    const float2 c2 = make_float2(cap2, cap2), n2 = make_float2(-2.f * cap2, -2.f * cap2);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][e]),
+                                                                    __uint_as_float(sv[c][e + 1])), k2);
+                            const float2 d = __fadd2_rn(
+                                make_float2(dec::fast_exp2(y.x), dec::fast_exp2(y.y)),
+                                make_float2(1.f, 1.f));
+                            const float2 s2 = __ffma2_rn(
+                                n2, make_float2(dec::fast_rcp(d.x), dec::fast_rcp(d.y)), c2);
+                            sv[c][e] = __float_as_uint(s2.x);
+                            sv[c][e + 1] = __float_as_uint(s2.y);
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * row_qs);
+                }
+                if (p.slopes != nullptr) {
+                    const float d0 = (float)(t0 - pos);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            sv[c][e] = __float_as_uint(fmaf(-slope2, fabsf(d0 + (float)(32 * c + e)),
+                                                            __uint_as_float(sv[c][e])));
+                }
+                if (t0 < lo) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (t0 + 32 * c + e < lo) sv[c][e] = __float_as_uint(-CUDART_INF_F);
+                }
             }
             // causal / length mask: tokens past `lim` do not exist for this row
             if (t0 + BN - 1 > lim) {
@@ -880,10 +1001,11 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             // the last tile: zero V rows past the sequence end (P is 0 there,
             // but 0 x NaN from an unwritten row would poison the product);
             // each stream zeroes before its own PV (both write the same zeros)
-            if (j * BN + BN > L) {
+            // (MOD: rows that no query of the CTA sees, at both ends)
+            if (t0 + BN > vend || (MOD && t0 < vbeg)) {
                 ok = wait_warp(bar(BAR_VF + j % VST), (j / VST) & 1);
                 if (!ok) break;
-                const int r0 = max(L - j * BN, 0);
+                const int r0 = max(vend - t0, 0);
                 unsigned char* vt = smem + OFF_V + (uint32_t)(j % VST) * KVTILE;
                 const int nchunks = (BN - r0) * 16;     // 16-byte chunks in both halves
                 for (int i = stid; i < nchunks; i += NSOFT * 32) {
@@ -891,6 +1013,10 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                     *reinterpret_cast<uint4*>(vt + (ch >> 3) * KVHALF + row * 128 + (ch & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
+                if constexpr (MOD)
+                    for (int i = stid; i < min(vbeg - t0, BN) * 16; i += NSOFT * 32)
+                        *reinterpret_cast<uint4*>(vt + ((i & 15) >> 3) * KVHALF + (i >> 4) * 128 +
+                                                  (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 dec::fence_proxy_async();
             }
             // PV_{j-1} done: the P columns are free and O holds tile j-1's sum;
@@ -938,7 +1064,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    w[e] = have_o ? H16<T>::pack(__uint_as_float(ov[2 * e]) * inv,
+                    w[e] = have_o && (!MOD || l > 0.f) ? H16<T>::pack(__uint_as_float(ov[2 * e]) * inv,
                                                  __uint_as_float(ov[2 * e + 1]) * inv)
                                   : 0u;
                 uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);

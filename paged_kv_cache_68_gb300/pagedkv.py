@@ -40,6 +40,14 @@ DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 KV_FP8_E4M3, KV_INT8 = 3, 4
 CACHE_CODE = {"fp8_e4m3": KV_FP8_E4M3, "int8": KV_INT8}
 
+
+class ScoreMods(ctypes.Structure):
+    """``kv_score_mods``: cap, distance bias and masks of scored attention."""
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int), ("first_visible", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
 
@@ -72,6 +80,7 @@ def load(build: bool = True) -> ctypes.CDLL:
         sig = {
             "kv_pool_create": ([I, I, I, I, I, P, P, ctypes.POINTER(P)], I),
             "kv_pool_create_quantized": ([I, I, I, I, I, I, P, P, P, P, F, F, ctypes.POINTER(P)], I),
+            "kv_pool_create_block_scaled": ([I, I, I, I, I, I, P, P, P, P, ctypes.POINTER(P)], I),
             "kv_pool_destroy": ([P], I),
             "kv_plan_step": ([P, P, P, I, P, I, P, I, P, P, P, P, P, P, I, P], I),
             "kv_append": ([P, P, P, P, I, P], I),
@@ -79,6 +88,11 @@ def load(build: bool = True) -> ctypes.CDLL:
             "paged_attention_workspace_size": ([P, I, I, ctypes.POINTER(S)], I),
             "paged_attention_decode_launches": ([P, I, I, ctypes.POINTER(I)], I),
             "paged_attention_decode": ([P, P, P, P, I, P, I, I, F, I, P, S, P], I),
+            "paged_attention_scored_workspace_size": ([P, I, I, ctypes.POINTER(S)], I),
+            "paged_attention_decode_scored": ([P, P, P, P, I, P, I, I, F, I,
+                                               ctypes.POINTER(ScoreMods), P, S, P], I),
+            "paged_attention_prefill_scored": ([P, P, P, P, I, I, P, I, P, I, I, F, I,
+                                                ctypes.POINTER(ScoreMods), P], I),
             "paged_attention_cascade_workspace_size": ([P, I, I, I, ctypes.POINTER(S)], I),
             "paged_attention_decode_cascade": ([P, P, P, P, I, P, I, I, F, I, P, P, P, I, P, S, P], I),
             "kv_swap_blocks": ([P, P, P, P, P, I, P, I, I, P], I),
@@ -178,6 +192,31 @@ def kv_pool_create_quantized(k_codes: torch.Tensor, v_codes: torch.Tensor, dtype
         n, bs, hkv, d, CACHE_CODE[cache], DTYPE_CODE[dtype], _dev(k_codes, "k_codes", torch.uint8),
         _dev(v_codes, "v_codes", torch.uint8), ks, vs, float(k_scale), float(v_scale),
         ctypes.byref(h)), "kv_pool_create_quantized")
+    return h
+
+
+def kv_pool_create_block_scaled(k_codes: torch.Tensor, v_codes: torch.Tensor, dtype, cache: str,
+                                k_scales: torch.Tensor, v_scales: torch.Tensor) -> ctypes.c_void_p:
+    """Describe an 8-bit pool with one scale per block and KV head: uint8 codes
+    [num_blocks, block_size, num_kv_heads, head_dim], fp32 scales [num_blocks,
+    num_kv_heads]; ``cache`` "fp8_e4m3" or "int8"; ``dtype`` the 16-bit type of
+    q, out and new K/V rows."""
+    if k_codes.shape != v_codes.shape or k_codes.dim() != 4:
+        raise ValueError("k_codes and v_codes must be equal-shaped 4-D tensors")
+    if cache not in CACHE_CODE:
+        raise ValueError(f"unknown cache format {cache!r}")
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    n, bs, hkv, d = k_codes.shape
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t is None or tuple(t.shape) != (n, hkv):
+            raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
+    _same_device(k_codes, v_codes, k_scales, v_scales)
+    h = ctypes.c_void_p()
+    _check(load().kv_pool_create_block_scaled(
+        n, bs, hkv, d, CACHE_CODE[cache], DTYPE_CODE[dtype], _dev(k_codes, "k_codes", torch.uint8),
+        _dev(v_codes, "v_codes", torch.uint8), _dev(k_scales, "k_scales", torch.float32),
+        _dev(v_scales, "v_scales", torch.float32), ctypes.byref(h)), "kv_pool_create_block_scaled")
     return h
 
 
@@ -283,6 +322,75 @@ def paged_attention_decode(handle, q, out, block_tables, seq_lens, scale: float,
         _stream(stream)), "paged_attention_decode")
 
 
+def _score_mods(num_q_heads: int, queries: int, softcap: float, alibi_slopes, window: int,
+                first_visible, batch: int = 0, prefix_lens=None) -> ScoreMods:
+    if alibi_slopes is not None:
+        _shape(alibi_slopes, "alibi_slopes", num_q_heads)
+    if first_visible is not None:
+        _shape(first_visible, "first_visible", queries)
+    if prefix_lens is not None:
+        _shape(prefix_lens, "prefix_lens", batch)
+    opt = lambda t, n, dt: None if t is None else _dev(t, n, dt)
+    return ScoreMods(float(softcap), opt(alibi_slopes, "alibi_slopes", torch.float32), int(window),
+                     opt(first_visible, "first_visible", torch.int32),
+                     opt(prefix_lens, "prefix_lens", torch.int32))
+
+
+def paged_attention_scored_workspace_size(handle, batch: int, num_q_heads: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().paged_attention_scored_workspace_size(handle, batch, num_q_heads,
+                                                        ctypes.byref(out)),
+           "paged_attention_scored_workspace_size")
+    return int(out.value)
+
+
+def paged_attention_decode_scored(handle, q, out, block_tables, seq_lens, scale: float,
+                                  num_kv_heads: int, workspace, dtype, *, softcap: float = 0.0,
+                                  alibi_slopes=None, window: int = 0, first_visible=None,
+                                  stream=None) -> None:
+    """``paged_attention_decode`` with tanh-capped scores (``softcap`` > 0), a
+    bias -alibi_slopes[h] * distance (fp32 [Hq]), a ``window`` over the last
+    positions and a first visible position per sequence (int32 [B])."""
+    b, hq, _ = q.shape
+    _same_device(q, out, block_tables, seq_lens, workspace, alibi_slopes, first_visible)
+    _shape(out, "out", *q.shape)
+    _shape(seq_lens, "seq_lens", b)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError(f"block_tables must be [{b}, max_blocks]")
+    mods = _score_mods(hq, b, softcap, alibi_slopes, window, first_visible)
+    _check(load().paged_attention_decode_scored(
+        handle, _dev(q, "q", dtype), _dev(out, "out", dtype),
+        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+        _dev(seq_lens, "seq_lens", torch.int32), int(b), int(hq), float(scale), int(num_kv_heads),
+        ctypes.byref(mods), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)),
+        "paged_attention_decode_scored")
+
+
+def paged_attention_prefill_scored(handle, q, out, cu_seqlens, max_query_len: int, block_tables,
+                                   seq_lens, scale: float, num_kv_heads: int, dtype, *,
+                                   softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                                   first_visible=None, prefix_lens=None, stream=None) -> None:
+    """``paged_attention_prefill`` with the cap, bias and masks of
+    ``paged_attention_decode_scored`` (first_visible int32 [T], one per query) and
+    a prefix of each request that all its queries see (prefix_lens int32 [B])."""
+    t, hq, _ = q.shape
+    b = int(seq_lens.numel())
+    _same_device(q, out, cu_seqlens, block_tables, seq_lens, alibi_slopes, first_visible,
+                 prefix_lens)
+    _shape(out, "out", *q.shape)
+    _shape(cu_seqlens, "cu_seqlens", b + 1)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError(f"block_tables must be [{b}, max_blocks]")
+    mods = _score_mods(hq, t, softcap, alibi_slopes, window, first_visible, b, prefix_lens)
+    _check(load().paged_attention_prefill_scored(
+        handle, _dev(q, "q", dtype), _dev(out, "out", dtype),
+        _dev(cu_seqlens, "cu_seqlens", torch.int32), int(t), int(max_query_len),
+        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+        _dev(seq_lens, "seq_lens", torch.int32), b, int(hq), float(scale), int(num_kv_heads),
+        ctypes.byref(mods), _stream(stream)), "paged_attention_prefill_scored")
+
+
 def paged_attention_cascade_workspace_size(handle, batch: int, num_q_heads: int,
                                            num_groups: int) -> int:
     out = ctypes.c_size_t()
@@ -349,10 +457,17 @@ class KVPool:
     def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, *, cache: Optional[str] = None,
                  dtype=None, k_scales: Optional[torch.Tensor] = None,
                  v_scales: Optional[torch.Tensor] = None, k_scale: float = 1.0,
-                 v_scale: float = 1.0):
+                 v_scale: float = 1.0, scale_per: Optional[str] = None):
         """A 16-bit or fp32 pool (k_pool, v_pool of that type), or with
         ``cache`` set an 8-bit pool: uint8 codes, ``dtype`` the 16-bit type of
-        q / out / new rows, and the scales ``kv_pool_create_quantized`` takes."""
+        q / out / new rows, and the scales ``kv_pool_create_quantized`` takes,
+        or with ``scale_per="block"`` k_scales and v_scales [num_blocks,
+        num_kv_heads] (``kv_pool_create_block_scaled``)."""
+        if scale_per not in (None, "block"):
+            raise ValueError(f"unknown scale_per {scale_per!r}")
+        if scale_per == "block" and cache is None:
+            raise ValueError("block scales belong to an 8-bit pool: give cache")
+        self.scale_per = scale_per
         self.k_pool, self.v_pool = k_pool, v_pool
         self.cache = cache
         self.k_scales, self.v_scales = k_scales, v_scales
@@ -360,6 +475,10 @@ class KVPool:
         if cache is None:
             self.dtype = k_pool.dtype
             self.handle = kv_pool_create(k_pool, v_pool)
+        elif scale_per == "block":
+            self.dtype = dtype
+            self.handle = kv_pool_create_block_scaled(k_pool, v_pool, dtype, cache, k_scales,
+                                                      v_scales)
         else:
             self.dtype = dtype
             self.handle = kv_pool_create_quantized(k_pool, v_pool, dtype, cache, k_scales,
@@ -401,13 +520,14 @@ class KVPool:
 
     def host_pool(self, num_host_blocks: int):
         """Pinned host arrays of this pool's layout for swapped-out blocks:
-        (k, v, k_scales, v_scales); the scales are None unless INT8."""
+        (k, v, k_scales, v_scales); the scales are None unless INT8 or per block."""
         shape = (num_host_blocks, self.block_size, self.num_kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=self.k_pool.dtype, pin_memory=True)
         v = torch.empty(shape, dtype=self.k_pool.dtype, pin_memory=True)
         ks = vs = None
-        if self.cache == "int8":
-            sshape = (num_host_blocks, self.num_kv_heads, self.block_size)
+        if self.cache == "int8" or self.scale_per == "block":
+            sshape = (num_host_blocks, self.num_kv_heads) + \
+                (() if self.scale_per == "block" else (self.block_size,))
             ks = torch.empty(sshape, dtype=torch.float32, pin_memory=True)
             vs = torch.empty(sshape, dtype=torch.float32, pin_memory=True)
         return k, v, ks, vs
@@ -436,6 +556,28 @@ class KVPool:
                                self.num_kv_heads, workspace, self.dtype, stream)
         return out
 
+    def scored_workspace(self, batch: int, num_q_heads: int) -> torch.Tensor:
+        """A cached device workspace large enough for ``decode_scored``."""
+        need = paged_attention_scored_workspace_size(self.handle, batch, num_q_heads)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_pool.device)
+        return self._ws
+
+    def decode_scored(self, q, block_tables, seq_lens, scale: float, *, softcap: float = 0.0,
+                      alibi_slopes=None, window: int = 0, first_visible=None, out=None,
+                      workspace=None, stream=None) -> torch.Tensor:
+        """Decode with capped or biased scores and masks
+        (``paged_attention_decode_scored``)."""
+        if out is None:
+            out = _new(q.shape, q.dtype, q.device, stream)
+        if workspace is None:
+            workspace = self.scored_workspace(q.shape[0], q.shape[1])
+        paged_attention_decode_scored(self.handle, q, out, block_tables, seq_lens, scale,
+                                      self.num_kv_heads, workspace, self.dtype, softcap=softcap,
+                                      alibi_slopes=alibi_slopes, window=window,
+                                      first_visible=first_visible, stream=stream)
+        return out
+
     def decode_cascade(self, q, block_tables, seq_lens, scale: float, groups, out=None,
                        workspace=None, stream=None) -> torch.Tensor:
         """Decode with shared-prefix groups: ``groups`` int32 [K, 3] on the
@@ -462,6 +604,20 @@ class KVPool:
             out = torch.empty_like(q)
         paged_attention_prefill(self.handle, q, out, cu_seqlens, max_query_len, block_tables,
                                 seq_lens, scale, self.num_kv_heads, self.dtype, stream)
+        return out
+
+    def prefill_scored(self, q, cu_seqlens, max_query_len: int, block_tables, seq_lens,
+                       scale: float, *, softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                       first_visible=None, prefix_lens=None, out=None, stream=None) -> torch.Tensor:
+        """Chunked prefill with capped or biased scores and masks
+        (``paged_attention_prefill_scored``)."""
+        if out is None:
+            out = _new(q.shape, q.dtype, q.device, stream)
+        paged_attention_prefill_scored(self.handle, q, out, cu_seqlens, max_query_len,
+                                       block_tables, seq_lens, scale, self.num_kv_heads,
+                                       self.dtype, softcap=softcap, alibi_slopes=alibi_slopes,
+                                       window=window, first_visible=first_visible,
+                                       prefix_lens=prefix_lens, stream=stream)
         return out
 
     def set_wait_limit(self, limit_ns: int) -> None:
