@@ -53,6 +53,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "pagedkv_internal.cuh"
@@ -65,6 +66,11 @@ constexpr int NTHREADS = (NCW + 1) * 32;     // + one producer warp (prefix pass
 constexpr int SPLIT_THREADS = NCW * 32;      // split kernel: the consumer warps load too
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMinChunk = 8;                 // fewest units a CTA is given
+// Scored decode merges in the split kernel, whatever the grid, while no (b, g)
+// can have more units (its extra cost included) than this: at kMinChunk units
+// a range, a handful of partials that one warp folds faster than a second
+// launch starts.
+constexpr int kFewUnits = 48;
 
 struct Params {
     const void* q;
@@ -2193,12 +2199,29 @@ __global__ void __launch_bounds__(SPLIT_THREADS) paged_decode_merge(const Params
 }
 
 // ------------------------------------------------------------- host side --
+// The dynamic shared memory a kernel may ask for, raised when a call needs
+// more than the largest so far on the current device, never lowered (one
+// runtime call the first time instead of one per launch).
+template <auto Kernel>
+cudaError_t allow_smem(int device, size_t bytes) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> allowed[kDevices];
+    if (device >= 0 && device < kDevices && allowed[device].load() >= (int)bytes) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && device >= 0 && device < kDevices) {
+        // (two threads may race here: a stale smaller note only costs a call)
+        int seen = allowed[device].load();
+        while (seen < (int)bytes && !allowed[device].compare_exchange_weak(seen, (int)bytes)) {}
+    }
+    return e;
+}
+
 template <typename T, int D, int G, class Pol>
 cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
                          cudaStream_t stream) {
     auto split = paged_decode_split<T, D, G, Pol>;
-    cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)plan.smem_bytes);
+    cudaError_t e = allow_smem<paged_decode_split<T, D, G, Pol>>(pool.device, plan.smem_bytes);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = call.q;
@@ -2218,7 +2241,14 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     p.num_blocks = pool.num_blocks;
     p.bs = pool.block_size;
     p.stages = plan.stages;
-    p.num_ctas = plan.num_ctas;
+    // No more CTAs than ranges of kMinChunk units (the smallest range) that the
+    // tables can hold: fewer sequences cut exactly as on the full grid, without
+    // the CTAs that would find no work.
+    const int pairs = call.batch * pool.num_kv_heads;
+    const long long most = (long long)pairs * ((call.max_blocks + Pol::kUnitBlocks - 1) /
+                                               Pol::kUnitBlocks + kPieceCost);
+    const long long ranges = (most + kMinChunk - 1) / kMinChunk;
+    p.num_ctas = (int)std::min<long long>(plan.num_ctas, (ranges + NCW - 1) / NCW);
     p.qscale = call.scale * 1.4426950408889634f;
     p.wait_ns = pool.wait_ns;
     p.g_first = call.g_first;
@@ -2237,7 +2267,7 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     p.window = call.mods ? call.mods->window : 0;
     p.first = call.mods ? call.mods->first_visible : nullptr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.num_ctas);
+    cfg.gridDim = dim3(p.num_ctas);
     cfg.blockDim = dim3(SPLIT_THREADS);
     cfg.dynamicSmemBytes = plan.smem_bytes;
     cfg.stream = stream;
@@ -2247,8 +2277,9 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // where the partials of cut (b, g) merge: in this kernel or a second one
-    const int pairs = call.batch * pool.num_kv_heads;
     p.merge_wpp = merge_warps_per_pair(plan.num_ctas * NCW, pairs);
+    if (Pol::kMod && (long long)p.num_ctas * NCW * kMinChunk >= most && most <= kFewUnits * (long long)pairs)
+        p.merge_wpp = 0;
     if (Pol::kH2)
         e = cudaLaunchKernelEx(&cfg, split, pool.tmap_k_h2, pool.tmap_v_h2, p);
     else if (Pol::kSwizzled)
@@ -2265,16 +2296,16 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
                                                       pool.num_sms * 4)));
     cfg.dynamicSmemBytes = merge_smem;
     if (merge_smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(merge, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+        e = allow_smem<paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod>>(pool.device, merge_smem);
         if (e != cudaSuccess) return e;
     }
     return cudaLaunchKernelEx(&cfg, merge, p);
 }
 
 template <typename T, int D, int G, class Pol>
-cudaError_t attrs_typed(size_t smem, int* ctas_per_sm) {
+cudaError_t attrs_typed(int device, size_t smem, int* ctas_per_sm) {
     auto split = paged_decode_split<T, D, G, Pol>;
-    cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<paged_decode_split<T, D, G, Pol>>(device, smem);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, split, SPLIT_THREADS, smem);
 }
@@ -2333,8 +2364,8 @@ template <typename T, int D, int G, class Pol> struct LaunchFn {
     }
 };
 template <typename T, int D, int G, class Pol> struct AttrsFn {
-    static cudaError_t run(size_t smem, int* ctas_per_sm) {
-        return attrs_typed<T, D, G, Pol>(smem, ctas_per_sm);
+    static cudaError_t run(int device, size_t smem, int* ctas_per_sm) {
+        return attrs_typed<T, D, G, Pol>(device, smem, ctas_per_sm);
     }
 };
 
@@ -2357,7 +2388,7 @@ cudaError_t attrs(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm)
     const bool tc = use_tensor_cores(pool, group);
 #define PKV_CASE(DD, GG)                                                                        \
     if (pool.head_dim == DD && group == GG)                                                     \
-        return with_policy<T, DD, GG, MOD, AttrsFn>(pool.block_size, tc, smem, ctas_per_sm);
+        return with_policy<T, DD, GG, MOD, AttrsFn>(pool.block_size, tc, pool.device, smem, ctas_per_sm);
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)
     PKV_CASE(128, 1) PKV_CASE(128, 2) PKV_CASE(128, 4) PKV_CASE(128, 8)
 #undef PKV_CASE
@@ -2412,7 +2443,7 @@ cudaError_t dispatch_q8(const kv_pool& pool, const DecodeCall& call, const Decod
 
 template <typename T, int SC = kScPlain, bool MOD = false>
 cudaError_t attrs_q8(const kv_pool& pool, int group, size_t smem, int* ctas_per_sm) {
-    return by_format<T, SC, MOD, AttrsFn>(pool, group, smem, ctas_per_sm);
+    return by_format<T, SC, MOD, AttrsFn>(pool, group, pool.device, smem, ctas_per_sm);
 }
 
 }  // namespace dec

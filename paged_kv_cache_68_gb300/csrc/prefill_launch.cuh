@@ -47,8 +47,7 @@ cudaError_t launch_typed(const kv_pool& pool, const PrefillCall& c, cudaStream_t
     }
     auto kern = paged_prefill<T, G, FMT, SC, MOD>;
     constexpr uint32_t smem_bytes = Lay<Q8>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem_bytes);
+    cudaError_t e = dec::allow_smem<paged_prefill<T, G, FMT, SC, MOD>>(pool.device, smem_bytes);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = c.q;

@@ -68,6 +68,8 @@ def library_path() -> str:
 def load(build: bool = True) -> ctypes.CDLL:
     """Load ``libpagedkv.so`` (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -115,12 +117,12 @@ def _check(status: int, what: str) -> None:
         raise PagedKVError(status, what)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -133,14 +135,20 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     return t.data_ptr()
 
 
-def _same_device(*tensors) -> None:
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+def _ptr(t: torch.Tensor, name: str, dtype, device: int) -> int:
+    """Address of a contiguous CUDA tensor of ``dtype`` on device ``device``."""
+    if t.get_device() != device or t.dtype != dtype or not t.is_contiguous():
+        _dev(t, name, dtype)
+        raise ValueError(f"tensors on different devices: {name} on {t.device}, not cuda:{device}")
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtype, device: int):
+    return None if t is None else _ptr(t, name, dtype, device)
 
 
 def _shape(t, name: str, *shape) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -211,12 +219,12 @@ def kv_pool_create_block_scaled(k_codes: torch.Tensor, v_codes: torch.Tensor, dt
     for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
         if t is None or tuple(t.shape) != (n, hkv):
             raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
-    _same_device(k_codes, v_codes, k_scales, v_scales)
+    dev, u8, f32 = k_codes.get_device(), torch.uint8, torch.float32
     h = ctypes.c_void_p()
     _check(load().kv_pool_create_block_scaled(
-        n, bs, hkv, d, CACHE_CODE[cache], DTYPE_CODE[dtype], _dev(k_codes, "k_codes", torch.uint8),
-        _dev(v_codes, "v_codes", torch.uint8), _dev(k_scales, "k_scales", torch.float32),
-        _dev(v_scales, "v_scales", torch.float32), ctypes.byref(h)), "kv_pool_create_block_scaled")
+        n, bs, hkv, d, CACHE_CODE[cache], DTYPE_CODE[dtype], _dev(k_codes, "k_codes", u8),
+        _ptr(v_codes, "v_codes", u8, dev), _ptr(k_scales, "k_scales", f32, dev),
+        _ptr(v_scales, "v_scales", f32, dev), ctypes.byref(h)), "kv_pool_create_block_scaled")
     return h
 
 
@@ -238,28 +246,28 @@ def kv_plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free
     """context_lens, new_lens int32 [B]; block_tables int32 [B, max_blocks]
     (updated in place); free_blocks int32 [F], free_head int32 [1]; the results
     go into ``plan``."""
-    _same_device(context_lens, new_lens, block_tables, free_blocks, free_head, *plan)
-    b, t = int(context_lens.numel()), int(plan.slot_mapping.numel())
+    (b,), (t,) = context_lens.shape, plan.slot_mapping.shape
     _shape(new_lens, "new_lens", b)
-    _shape(context_lens, "context_lens", b)
     if block_tables.dim() != 2 or block_tables.shape[0] != b:
         raise ValueError(f"block_tables must be [{b}, max_blocks]")
     _shape(free_head, "free_head", 1)
     _shape(plan.free_head, "plan.free_head", 1)
     _shape(plan.cu_seqlens, "plan.cu_seqlens", b + 1)
     _shape(plan.seq_lens, "plan.seq_lens", b)
-    if plan.positions is not None:
-        _shape(plan.positions, "plan.positions", t)
-    i32 = lambda x, n: _dev(x, n, torch.int32)
+    dev, i32 = context_lens.get_device(), torch.int32
+    pos = plan.positions
+    if pos is not None:
+        _shape(pos, "plan.positions", t)
     _check(load().kv_plan_step(
-        handle, i32(context_lens, "context_lens"), i32(new_lens, "new_lens"), b,
-        i32(block_tables, "block_tables"), int(block_tables.shape[1]),
-        i32(free_blocks, "free_blocks"), int(free_blocks.numel()), i32(free_head, "free_head"),
-        i32(plan.free_head, "plan.free_head"), i32(plan.cu_seqlens, "plan.cu_seqlens"),
-        i32(plan.seq_lens, "plan.seq_lens"),
-        _dev(plan.slot_mapping, "plan.slot_mapping", torch.int64),
-        None if plan.positions is None else i32(plan.positions, "plan.positions"), t,
-        _stream(stream)), "kv_plan_step")
+        handle, _ptr(context_lens, "context_lens", i32, dev), _ptr(new_lens, "new_lens", i32, dev), b,
+        _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _ptr(free_blocks, "free_blocks", i32, dev), free_blocks.numel(),
+        _ptr(free_head, "free_head", i32, dev), _ptr(plan.free_head, "plan.free_head", i32, dev),
+        _ptr(plan.cu_seqlens, "plan.cu_seqlens", i32, dev),
+        _ptr(plan.seq_lens, "plan.seq_lens", i32, dev),
+        _ptr(plan.slot_mapping, "plan.slot_mapping", torch.int64, dev),
+        None if pos is None else _ptr(pos, "plan.positions", i32, dev), t, _stream(stream)),
+        "kv_plan_step")
 
 
 def kv_append(handle, k_new, v_new, slot_mapping, dtype, stream=None) -> None:
@@ -322,18 +330,19 @@ def paged_attention_decode(handle, q, out, block_tables, seq_lens, scale: float,
         _stream(stream)), "paged_attention_decode")
 
 
-def _score_mods(num_q_heads: int, queries: int, softcap: float, alibi_slopes, window: int,
+def _score_mods(num_q_heads: int, queries: int, dev: int, softcap: float, alibi_slopes, window: int,
                 first_visible, batch: int = 0, prefix_lens=None) -> ScoreMods:
+    m = ScoreMods(softcap, None, window, None, None)
     if alibi_slopes is not None:
         _shape(alibi_slopes, "alibi_slopes", num_q_heads)
+        m.alibi_slopes = _ptr(alibi_slopes, "alibi_slopes", torch.float32, dev)
     if first_visible is not None:
         _shape(first_visible, "first_visible", queries)
+        m.first_visible = _ptr(first_visible, "first_visible", torch.int32, dev)
     if prefix_lens is not None:
         _shape(prefix_lens, "prefix_lens", batch)
-    opt = lambda t, n, dt: None if t is None else _dev(t, n, dt)
-    return ScoreMods(float(softcap), opt(alibi_slopes, "alibi_slopes", torch.float32), int(window),
-                     opt(first_visible, "first_visible", torch.int32),
-                     opt(prefix_lens, "prefix_lens", torch.int32))
+        m.prefix_lens = _ptr(prefix_lens, "prefix_lens", torch.int32, dev)
+    return m
 
 
 def paged_attention_scored_workspace_size(handle, batch: int, num_q_heads: int) -> int:
@@ -352,17 +361,17 @@ def paged_attention_decode_scored(handle, q, out, block_tables, seq_lens, scale:
     bias -alibi_slopes[h] * distance (fp32 [Hq]), a ``window`` over the last
     positions and a first visible position per sequence (int32 [B])."""
     b, hq, _ = q.shape
-    _same_device(q, out, block_tables, seq_lens, workspace, alibi_slopes, first_visible)
+    dev, i32 = q.get_device(), torch.int32
     _shape(out, "out", *q.shape)
     _shape(seq_lens, "seq_lens", b)
     if block_tables.dim() != 2 or block_tables.shape[0] != b:
         raise ValueError(f"block_tables must be [{b}, max_blocks]")
-    mods = _score_mods(hq, b, softcap, alibi_slopes, window, first_visible)
+    mods = _score_mods(hq, b, dev, softcap, alibi_slopes, window, first_visible)
     _check(load().paged_attention_decode_scored(
-        handle, _dev(q, "q", dtype), _dev(out, "out", dtype),
-        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
-        _dev(seq_lens, "seq_lens", torch.int32), int(b), int(hq), float(scale), int(num_kv_heads),
-        ctypes.byref(mods), _dev(workspace, "workspace"),
+        handle, _ptr(q, "q", dtype, dev), _ptr(out, "out", dtype, dev),
+        _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _ptr(seq_lens, "seq_lens", i32, dev), b, hq, scale, num_kv_heads, ctypes.byref(mods),
+        _ptr(workspace, "workspace", workspace.dtype, dev),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "paged_attention_decode_scored")
 
@@ -375,20 +384,19 @@ def paged_attention_prefill_scored(handle, q, out, cu_seqlens, max_query_len: in
     ``paged_attention_decode_scored`` (first_visible int32 [T], one per query) and
     a prefix of each request that all its queries see (prefix_lens int32 [B])."""
     t, hq, _ = q.shape
-    b = int(seq_lens.numel())
-    _same_device(q, out, cu_seqlens, block_tables, seq_lens, alibi_slopes, first_visible,
-                 prefix_lens)
+    b = seq_lens.numel()
+    dev, i32 = q.get_device(), torch.int32
     _shape(out, "out", *q.shape)
     _shape(cu_seqlens, "cu_seqlens", b + 1)
     if block_tables.dim() != 2 or block_tables.shape[0] != b:
         raise ValueError(f"block_tables must be [{b}, max_blocks]")
-    mods = _score_mods(hq, t, softcap, alibi_slopes, window, first_visible, b, prefix_lens)
+    mods = _score_mods(hq, t, dev, softcap, alibi_slopes, window, first_visible, b, prefix_lens)
     _check(load().paged_attention_prefill_scored(
-        handle, _dev(q, "q", dtype), _dev(out, "out", dtype),
-        _dev(cu_seqlens, "cu_seqlens", torch.int32), int(t), int(max_query_len),
-        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
-        _dev(seq_lens, "seq_lens", torch.int32), b, int(hq), float(scale), int(num_kv_heads),
-        ctypes.byref(mods), _stream(stream)), "paged_attention_prefill_scored")
+        handle, _ptr(q, "q", dtype, dev), _ptr(out, "out", dtype, dev),
+        _ptr(cu_seqlens, "cu_seqlens", i32, dev), t, max_query_len,
+        _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _ptr(seq_lens, "seq_lens", i32, dev), b, hq, scale, num_kv_heads, ctypes.byref(mods),
+        _stream(stream)), "paged_attention_prefill_scored")
 
 
 def paged_attention_cascade_workspace_size(handle, batch: int, num_q_heads: int,
@@ -484,6 +492,7 @@ class KVPool:
             self.handle = kv_pool_create_quantized(k_pool, v_pool, dtype, cache, k_scales,
                                                    v_scales, k_scale, v_scale)
         self._ws: Optional[torch.Tensor] = None
+        self._scored_need = {}                  # workspace bytes by (batch, query heads)
 
     def close(self) -> None:
         if self.handle is not None:
@@ -501,12 +510,12 @@ class KVPool:
         """Block tables (in place), slots, positions, offsets and lengths of one
         step, built on the GPU; ``num_tokens`` sizes the token arrays."""
         if out is None:
-            dev, b = context_lens.device, int(context_lens.numel())
-            new = lambda n, dt: _new((n,), dt, dev, stream)
-            out = StepPlan(new(b + 1, torch.int32), new(b, torch.int32),
-                           new(num_tokens, torch.int64), new(num_tokens, torch.int32),
-                           new(1, torch.int32))
-        elif int(out.slot_mapping.numel()) != num_tokens:
+            dev, b = context_lens.device, context_lens.numel()
+            # one allocation for the int32 results
+            i32 = _new(num_tokens + 2 * b + 2, torch.int32, dev, stream)
+            pos, cu, lens, head = i32.split((num_tokens, b + 1, b, 1))
+            out = StepPlan(cu, lens, _new(num_tokens, torch.int64, dev, stream), pos, head)
+        elif out.slot_mapping.numel() != num_tokens:
             raise ValueError(f"out.slot_mapping must hold {num_tokens} tokens")
         kv_plan_step(self.handle, context_lens, new_lens, block_tables, free_blocks, free_head, out,
                      stream)
@@ -558,7 +567,10 @@ class KVPool:
 
     def scored_workspace(self, batch: int, num_q_heads: int) -> torch.Tensor:
         """A cached device workspace large enough for ``decode_scored``."""
-        need = paged_attention_scored_workspace_size(self.handle, batch, num_q_heads)
+        need = self._scored_need.get((batch, num_q_heads))
+        if need is None:
+            need = paged_attention_scored_workspace_size(self.handle, batch, num_q_heads)
+            self._scored_need[batch, num_q_heads] = need
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_pool.device)
         return self._ws
@@ -569,7 +581,7 @@ class KVPool:
         """Decode with capped or biased scores and masks
         (``paged_attention_decode_scored``)."""
         if out is None:
-            out = _new(q.shape, q.dtype, q.device, stream)
+            out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
         if workspace is None:
             workspace = self.scored_workspace(q.shape[0], q.shape[1])
         paged_attention_decode_scored(self.handle, q, out, block_tables, seq_lens, scale,
@@ -612,7 +624,7 @@ class KVPool:
         """Chunked prefill with capped or biased scores and masks
         (``paged_attention_prefill_scored``)."""
         if out is None:
-            out = _new(q.shape, q.dtype, q.device, stream)
+            out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
         paged_attention_prefill_scored(self.handle, q, out, cu_seqlens, max_query_len,
                                        block_tables, seq_lens, scale, self.num_kv_heads,
                                        self.dtype, softcap=softcap, alibi_slopes=alibi_slopes,
