@@ -133,8 +133,7 @@ struct Lay {
     static constexpr uint32_t cv = ck + (Q8 ? CST * CTILE : 0u);
     static constexpr uint32_t sc = cv + (Q8 ? CST * CTILE : 0u);       // [SCS][K, V][BN]
     static constexpr uint32_t csc = sc + (Q8 ? SCS * 2u * BN * 4u : 0u); // [K, V][CST][BN]
-    static constexpr uint32_t qinv = csc + (Q8 ? 2u * CST * BN * 4u : 0u); // [stream][BM] 2^-e
-    static constexpr uint32_t bar = qinv + (Q8 ? 2u * BM * 4u : 0u);
+    static constexpr uint32_t bar = csc + (Q8 ? 2u * CST * BN * 4u : 0u);
     static constexpr int nbars = Q8 ? NBARS_Q8 : NBARS;
     static constexpr uint32_t order = bar + 8u * nbars;
     static constexpr uint32_t tmem = order + 4u * (kMaxRanked + 4);
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             // INT8 scale ring: written by both producers, read by every softmax warp
             if (i >= BAR_SCF && i < BAR_SCF + SCS) count = 2;
             if (i >= BAR_SCE && i < BAR_SCE + SCS) count = (uint32_t)(NSOFT * nstreams);
-            if (i == BAR_QC) count = (uint32_t)nstreams;   // one producer per query tile
+            if (i == BAR_QC) count = (uint32_t)(NSOFT * nstreams);   // each softmax warp its rows
             dec::mbar_init(bar(i), count);
         }
         *abort_flag = 0;
@@ -592,59 +591,6 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                     codes_issued = jj + 1;
                 };
                 for (int jj = 0; jj < min(CST, ntiles); ++jj) issue_codes(jj);
-                if constexpr (QCONV) {
-                    // query tile x (the K producer stream A's, the V producer
-                    // B's) into f16 in place: lane takes rows lane + 32 k
-                    const int x = is_k ? 0 : 1;
-                    if (x < nstreams) {
-                        bool ok = true;
-                        if (lane == 0) ok = wait_or_abort(bar(BAR_Q), 0, abort_flag, p.err, p.wait_ns);
-                        if (__shfl_sync(FULL, ok ? 1 : 0, 0)) {
-                            unsigned char* qt = smem + OFF_Q + (uint32_t)x * QTILE;
-                            float* qinv = reinterpret_cast<float*>(smem + LY::qinv) + x * BM;
-#pragma unroll 1
-                            for (int k = 0; k < BM / 32; ++k) {
-                                const int r = lane + 32 * k;
-                                // the row's 16-byte chunk c: 64-dim half c / 8, chunk c % 8
-                                auto chunk = [&](int c) {
-                                    return reinterpret_cast<uint4*>(qt + (c >> 3) * QHALF + r * 128 +
-                                                                    (((c & 7) ^ (r & 7)) << 4));
-                                };
-                                float amax = 0.f;
-#pragma unroll 4
-                                for (int c = 0; c < 16; ++c) {
-                                    const uint4 w = *chunk(c);
-                                    const uint32_t e4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        amax = fmaxf(amax, fmaxf(fabsf(H16<T>::low(e4[e])),
-                                                                 fabsf(H16<T>::high(e4[e]))));
-                                }
-                                // 2^e with amax * 2^e in [2^14, 2^15): the exponent field of amax
-                                int ex2 = 0;
-                                if (amax > 0.f && amax <= 3.0e38f) {
-                                    const int ex = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 126;
-                                    ex2 = min(max(15 - ex, -120), 120);
-                                }
-                                const float up = __uint_as_float((uint32_t)(ex2 + 127) << 23);
-                                qinv[r] = __uint_as_float((uint32_t)(127 - ex2) << 23);
-#pragma unroll 4
-                                for (int c = 0; c < 16; ++c) {
-                                    const uint4 w = *chunk(c);
-                                    uint32_t e4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        e4[e] = H16<__half>::pack(H16<T>::low(e4[e]) * up,
-                                                                  H16<T>::high(e4[e]) * up);
-                                    *chunk(c) = make_uint4(e4[0], e4[1], e4[2], e4[3]);
-                                }
-                            }
-                            dec::fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) dec::mbar_arrive(bar(BAR_QC));
-                        }
-                    }
-                }
                 for (int j = 0; j < ntiles; ++j) {
                     const int slot = j % nst, cs = j % CST;
                     bool ok = true;
@@ -870,15 +816,55 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             return __all_sync(FULL, wait_or_abort(bb, parity, abort_flag, p.err, p.wait_ns));
         };
         if constexpr (QCONV) {
-            // the row's 2^-e, written with the converted query tile
+            // The row into f16 in place, times the power of two that puts its
+            // largest |q| into [2^14, 2^15); its scores then carry 2^-e.  (All
+            // the softmax warps, idle until the first scores; a producer warp
+            // doing it alone held the first tile back by 3-4 us.)
             if (ntiles > 0) {
-                ok = wait_warp(bar(BAR_QC), 0);
-                if (ok) qs *= reinterpret_cast<const float*>(smem + LY::qinv)[x * BM + r];
+                ok = wait_warp(bar(BAR_Q), 0);
+                if (ok) {
+                    unsigned char* qt = smem + OFF_Q + (uint32_t)x * QTILE;
+                    // the row's 16-byte chunk c: 64-dim half c / 8, chunk c % 8
+                    auto chunk = [&](int c) {
+                        return reinterpret_cast<uint4*>(qt + (c >> 3) * QHALF + r * 128 +
+                                                        (((c & 7) ^ (r & 7)) << 4));
+                    };
+                    float amax = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 w = *chunk(c);
+                        const uint32_t e4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            amax = fmaxf(amax, fmaxf(fabsf(H16<T>::low(e4[e])),
+                                                     fabsf(H16<T>::high(e4[e]))));
+                    }
+                    // 2^e with amax * 2^e in [2^14, 2^15): the exponent field of amax
+                    int ex2 = 0;
+                    if (amax > 0.f && amax <= 3.0e38f) {
+                        const int ex = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 126;
+                        ex2 = min(max(15 - ex, -120), 120);
+                    }
+                    const float up = __uint_as_float((uint32_t)(ex2 + 127) << 23);
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 w = *chunk(c);
+                        uint32_t e4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            e4[e] = H16<__half>::pack(H16<T>::low(e4[e]) * up,
+                                                      H16<T>::high(e4[e]) * up);
+                        *chunk(c) = make_uint4(e4[0], e4[1], e4[2], e4[3]);
+                    }
+                    qs *= __uint_as_float((uint32_t)(127 - ex2) << 23);
+                    dec::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) dec::mbar_arrive(bar(BAR_QC));
+                }
             }
         }
         // (MOD scales the scores before it caps and biases them)
         const float row_qs = qs;
-        if constexpr (MOD) qs = 1.f;
         for (int j = 0; ok && j < ntiles; ++j) {
             const int t0 = (jt0 + j) * BN;
             uint32_t sv[2][32];
@@ -896,24 +882,43 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             if constexpr (SCALES) {
                 ok = wait_warp(bar(BAR_SCF + j % SCS), (j / SCS) & 1);
                 if (!ok) break;
+            }
+            // block scales: 16 tokens lie in one block, so four K factors (MOD
+            // takes them with the softmax scale) and four V factors; a block past
+            // the sequence has no scale, and P is 0 there
+            float kf[4] = {1.f, 1.f, 1.f, 1.f}, vf[4] = {1.f, 1.f, 1.f, 1.f};
+            if constexpr (BLOCKSC) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kf[i] = tsc[16 * i];
+                    vf[i] = t0 + 16 * i < L ? tsc[BN + 16 * i] : 0.f;
+                }
+            }
+            if constexpr (SCALES && !(BLOCKSC && MOD)) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * tsc[32 * c + e]);
+                        sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) *
+                                                   (BLOCKSC ? kf[2 * c + e / 16] : tsc[32 * c + e]));
             }
             if constexpr (MOD) {
-                const float2 q2 = make_float2(row_qs, row_qs);
+                // (acc -> base-2 score, for the row's 16-token groups)
+                auto q2 = [&](int c, int e) {
+                    const float f = BLOCKSC ? row_qs * kf[2 * c + e / 16] : row_qs;
+                    return make_float2(f, f);
+                };
                 if (p.softcap > 0.f) {
                     const float cap2 = p.softcap * 1.4426950408889634f;
-                    const float2 k2 = __fmul2_rn(q2, make_float2(2.f * p.inv_softcap, 2.f * p.inv_softcap));
+                    const float2 i2 = make_float2(2.f * p.inv_softcap, 2.f * p.inv_softcap);
                     const float2 c2 = make_float2(cap2, cap2), n2 = make_float2(-2.f * cap2, -2.f * cap2);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][e]),
-                                                                    __uint_as_float(sv[c][e + 1])), k2);
+                                                                    __uint_as_float(sv[c][e + 1])),
+                                                        __fmul2_rn(q2(c, e), i2));
                             const float2 d = __fadd2_rn(
                                 make_float2(dec::fast_exp2(y.x), dec::fast_exp2(y.y)),
                                 make_float2(1.f, 1.f));
@@ -926,8 +931,13 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) * row_qs);
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][e]),
+                                                                    __uint_as_float(sv[c][e + 1])),
+                                                        q2(c, e));
+                            sv[c][e] = __float_as_uint(y.x);
+                            sv[c][e + 1] = __float_as_uint(y.y);
+                        }
                 }
                 if (p.slopes != nullptr) {
                     const float d0 = (float)(t0 - pos);
@@ -962,7 +972,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 for (int e = 2; e < 32; e += 2)
                     mx2[c] = max3(mx2[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
             }
-            const float m_new = fmaxf(m, fmaxf(mx2[0], mx2[1]) * qs);
+            const float m_new = fmaxf(m, MOD ? fmaxf(mx2[0], mx2[1]) : fmaxf(mx2[0], mx2[1]) * qs);
             float alpha = 1.f;
             const bool grow = m_new > m + kRescaleLog2;   // false while both are -inf
             if (grow) {
@@ -980,13 +990,16 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float2 xx = __ffma2_rn(
-                        make_float2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), qs2,
-                        nmu2);
+                    const float2 sc2 =
+                        make_float2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+                    const float2 xx = MOD ? __fadd2_rn(sc2, nmu2) : __ffma2_rn(sc2, qs2, nmu2);
                     const float2 pp = make_float2(dec::fast_exp2(xx.x), dec::fast_exp2(xx.y));
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], pp);
                     float2 pv = pp;
-                    if constexpr (SCALES) {
+                    if constexpr (BLOCKSC) {
+                        const float f = vf[2 * c + e / 16];
+                        pv = __fmul2_rn(pp, make_float2(f, f));
+                    } else if constexpr (SCALES) {
                         // P times the token's V scale (0 where P is: masked
                         // tokens' scales may be anything)
                         const float v0 = tsc[BN + 32 * c + e], v1 = tsc[BN + 32 * c + e + 1];
