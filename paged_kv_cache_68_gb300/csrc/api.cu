@@ -148,15 +148,24 @@ static DecodeUnit decode_unit(const kv_pool& pool, bool scored) {
 #undef PKV_UNIT
 }
 
+// Pool blocks per work unit of the decode kernels.
+static int decode_unit_blocks(const kv_pool& pool, int num_q_heads) {
+    const int G = num_q_heads / pool.num_kv_heads;
+    const bool pairs = is_q8(pool) ? dec::q8_pairs_blocks(pool, G)
+                                   : pool.block_size == 8 && dec::use_tensor_cores(pool, G);
+    return pairs ? 2 : 1;
+}
+
 cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups, bool scored,
-                        DecodePlan* plan) {
+                        DecodePlan* plan, bool deep) {
     {
         std::lock_guard<std::mutex> lock(pool.plan_mu);
-        if (pool.plan_batch == batch && pool.plan_hq == num_q_heads &&
-            pool.plan_groups == num_groups && pool.plan_scored == scored) {
-            *plan = pool.plan;
-            return cudaSuccess;
-        }
+        for (const auto& e : pool.plans)
+            if (e.batch == batch && e.hq == num_q_heads && e.groups == num_groups &&
+                e.scored == scored && e.deep == deep) {
+                *plan = e.plan;
+                return cudaSuccess;
+            }
     }
     const int G = num_q_heads / pool.num_kv_heads;
     const int D = pool.head_dim, elt = pool.elem_bytes;
@@ -164,9 +173,7 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
     // tokens per work unit: block size 8 on the tensor cores, and 8-bit pools
     // of block size 16 with groups of 4 or 8, pair two blocks (TcPolicy8x2,
     // Tc8Policy2); the kernel lays out its ring for the same unit size
-    const bool pairs = q8 ? dec::q8_pairs_blocks(pool, G)
-                          : pool.block_size == 8 && dec::use_tensor_cores(pool, G);
-    const int bs = pool.block_size * (pairs ? 2 : 1);
+    const int bs = pool.block_size * decode_unit_blocks(pool, num_q_heads);
     // scale bytes per tile row, or per stage
     const int sb = pool.cache_dtype == KV_INT8 && !pool.block_scales ? 4 : 0;
     const int stage_sb = pool.block_scales ? dec::kStageScales : 0;
@@ -193,7 +200,9 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
         const cudaError_t e = unit.attrs(pool, G, smem, &occ);
         if (e != cudaSuccess) return e;
         const int per_warp = S / ncw > max_per_warp ? max_per_warp : S / ncw;
-        const int score = occ * per_warp;
+        // (deep: few units, so the deepest ring on one CTA per SM)
+        if (deep && occ > 1) occ = 1;
+        const int score = deep ? S : occ * per_warp;
         if (occ >= 1 && score >= best_score) {
             best_s = S;
             best_occ = occ;
@@ -219,11 +228,14 @@ cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_group
     pl.ws_bytes = off;
     {
         std::lock_guard<std::mutex> lock(pool.plan_mu);
-        pool.plan = pl;
-        pool.plan_batch = batch;
-        pool.plan_hq = num_q_heads;
-        pool.plan_groups = num_groups;
-        pool.plan_scored = scored;
+        auto& e = pool.plans[pool.plan_next];
+        pool.plan_next = (pool.plan_next + 1) % 8;
+        e.batch = batch;
+        e.hq = num_q_heads;
+        e.groups = num_groups;
+        e.scored = scored;
+        e.deep = deep;
+        e.plan = pl;
     }
     *plan = pl;
     return cudaSuccess;
@@ -522,8 +534,19 @@ static kv_status decode_impl(kv_pool_t pool, const void* q, void* out,
         return KV_EUNSUPPORTED;
     if (!(scale == scale)) return KV_EINVAL;
     pagedkv::DecodePlan plan;
+    // scored calls whose pieces all have a warp at one CTA per SM: deep rings
+    bool deep = false;
+    if (mods) {
+        using namespace pagedkv::dec;
+        const int bsu = pool->block_size * pagedkv::decode_unit_blocks(*pool, num_q_heads);
+        const int most = scored_units(
+            *mods, (int)(((long long)max_blocks_per_seq * pool->block_size + bsu - 1) / bsu), bsu);
+        const int per = pagedkv::is_q8(*pool) || pool->block_size == 32 ? kPerLargeUnits : kPerUnits;
+        deep = (long long)batch * pool->num_kv_heads * ((most + per - 1) / per) <=
+               (long long)pool->num_sms * NCW;
+    }
     cudaError_t e =
-        pagedkv::plan_decode(*pool, batch, num_q_heads, num_groups, mods != nullptr, &plan);
+        pagedkv::plan_decode(*pool, batch, num_q_heads, num_groups, mods != nullptr, &plan, deep);
     if (e == cudaErrorNotSupported) return KV_EUNSUPPORTED;
     if (e != cudaSuccess) return pagedkv::cuda_fail(e, "paged_attention_decode(plan)");
     if (workspace_bytes < plan.ws_bytes) return KV_ENOWORKSPACE;

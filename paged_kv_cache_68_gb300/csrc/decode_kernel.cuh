@@ -67,10 +67,18 @@ constexpr int SPLIT_THREADS = NCW * 32;      // split kernel: the consumer warps
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMinChunk = 8;                 // fewest units a CTA is given
 // Scored decode merges in the split kernel, whatever the grid, while no (b, g)
-// can have more units (its extra cost included) than this: at kMinChunk units
-// a range, a handful of partials that one warp folds faster than a second
-// launch starts.
-constexpr int kFewUnits = 48;
+// has more pieces than this: a handful of partials that one warp folds faster
+// than a second launch starts.
+constexpr int kFewPieces = 12;
+// Its units per piece: four of up to 16 tokens, two of more (a tensor-core unit
+// costs a warp about 1 us per 16 tokens when nothing else runs beside it; 8 and 4
+// were slower at a 512-token window: 20.2 against 17.4 us a call).
+constexpr int kPerUnits = 4, kPerLargeUnits = 2;
+// The most units of `bsu` tokens that a sequence of at most `units` can see: a
+// window of w tokens touches (w - 1) / bsu + 2 of them at most.
+inline int scored_units(const kv_score_mods& mods, int units, int bsu) {
+    return mods.window > 0 ? std::min(units, (mods.window - 1) / bsu + 2) : units;
+}
 
 struct Params {
     const void* q;
@@ -120,7 +128,7 @@ struct Params {
 
 // ---------------------------------------------------------------- layout ---
 struct Layout {
-    uint32_t full, valid, misc, prefix, groups, skip, pst, pbuf, abuf, sring, ring;
+    uint32_t full, valid, misc, prefix, pieces, groups, skip, pst, pbuf, abuf, sring, ring;
     uint32_t pst_bytes, tx_bytes, stage_bytes, total;
     // elt: bytes per pool element; K: cascade groups (0 for plain decode);
     // sb: scale bytes per token row of a tile (INT8 pools: 4); stage_sb: scale
@@ -133,6 +141,7 @@ struct Layout {
         valid = off;  off += 4u * S;
         misc = off;   off += 4u * 40;            // abort flag + warp totals
         prefix = off; off += 4u * (B + 1);
+        pieces = off; off += skips ? 4u * (B + 1) : 0u;  // scored decode's pieces before each sequence
         groups = off; off += K > 0 ? 4u * 3u * K : 0u;   // used groups: first, size, blocks
         skip = off;   off += K > 0 || skips ? 4u * B : 0u;   // leading units each sequence skips
         off = (off + 15u) & ~15u;
@@ -544,6 +553,35 @@ struct WorkCut {
     }
 };
 
+// How scored decode cuts them.  While there are warps to spare (windows and short
+// contexts leave few units), what counts is one warp's latency: a second segment
+// in a warp's range costs 2-3 us, a cut 4-5 us (the partials, their count, their
+// merge), eight units of 16 tokens about as much.  So each segment is cut by
+// itself into pieces of `per` units, one warp each, when the grid has that many
+// warps; otherwise as above.
+struct ScoredCut {
+    WorkCut cut;
+    const int* pieces;     // [B + 1] pieces of KV head 0 before each sequence
+    int per;
+    bool aligned;
+    __device__ __forceinline__ ScoredCut(const int* pre, const int* pcs, int B, int H, int W, int per_)
+        : cut(pre, B, H, W), pieces(pcs), per(per_), aligned(pcs[B] * H <= W) {}
+    __device__ __forceinline__ int range_of(int u, int s) const {
+        if (!aligned) return cut.range_of(u, s);
+        const int H = cut.H, b = s / H, g = s - b * H;
+        const int seg = cut.prefix[b] * H + g * (cut.prefix[b + 1] - cut.prefix[b]);
+        return pieces[b] * H + g * (pieces[b + 1] - pieces[b]) + (u - seg) / per;
+    }
+    __device__ __forceinline__ int start_unit(int c) const {
+        if (!aligned) return cut.start_unit(c);
+        const int H = cut.H, B = cut.B;
+        if (c >= pieces[B] * H) return cut.prefix[B] * H;
+        const int b = find_seq(pieces, B, c, H);
+        const int k = pieces[b + 1] - pieces[b], r = c - pieces[b] * H, g = r / k;
+        return cut.prefix[b] * H + g * (cut.prefix[b + 1] - cut.prefix[b]) + (r - g * k) * per;
+    }
+};
+
 // ------------------------------------------------------- compute policies --
 // Both policies keep one warp's running softmax state for one (b, g) piece and
 // expose: begin (load the group's query rows), block (fold one KV block in),
@@ -636,6 +674,7 @@ struct CorePolicy {
     static constexpr int kScaleBytes = 0;
     static constexpr bool kBlockScales = false;
     static constexpr bool kMod = MOD;
+    static constexpr int kPer = kPerUnits;       // scored decode: units per piece (ScoredCut)
     static constexpr int kUnitBlocks = 1;        // pool blocks per work unit
 
     ScoreMods<MOD, 1, std::is_same<T, float>::value> mods;
@@ -841,6 +880,7 @@ struct TcPolicy {
     static constexpr int kScaleBytes = 0;
     static constexpr bool kBlockScales = false;
     static constexpr bool kMod = MOD;
+    static constexpr int kPer = BSC == 32 ? kPerLargeUnits : kPerUnits;
     static constexpr int kUnitBlocks = 1;  // pool blocks per work unit
     static constexpr int KS = D / 16;      // QK k-steps (16 dims each)
     static constexpr int MT = D / 16;      // PV m-tiles (16 dims each)
@@ -1203,6 +1243,7 @@ struct Tc8Policy : TcPolicy<T, D, G, 16, true, false, MOD> {
     static constexpr int kKvBytes = 1;
     static constexpr int kScaleBytes = SC == kScToken ? 4 : 0;
     static constexpr bool kBlockScales = SC == kScBlock;
+    static constexpr int kPer = kPerLargeUnits;  // (32 tokens a unit or more)
 
     float qs;             // scale * log2(e) * 2^-e (* the FP8 K scale)
     float vq;             // FP8: the V scale; INT8: 1
@@ -1447,6 +1488,37 @@ __device__ __forceinline__ void cas128(unsigned long long* p, unsigned long long
         : "l"(nlo), "l"(nhi), "l"(p)
         : "memory");
 }
+__device__ __forceinline__ void fence_acq_rel_gpu() {
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+}
+// Scored decode counts in two steps, off and on the critical path.  When a piece
+// begins, the counter is given the call's tag with a count of zero, unless it
+// has the tag (a replayed graph's, or another piece was first): the
+// compare-and-swap takes effect only on the stale value it read.  When the piece
+// is done, one atomic add counts it: pieces that end together do not wait on
+// each other's compare-and-swaps, which cost each about 1 us in a row (nine
+// pieces of one segment: 23.8 us a call counted that way).
+__device__ __forceinline__ void open_count(unsigned long long* ctr, unsigned long long tag) {
+    unsigned long long lo, hi;
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(lo), "=l"(hi) : "l"(ctr) : "memory");
+    while (lo != tag) {
+        const unsigned long long elo = lo, ehi = hi;
+        cas128(ctr, lo, hi, tag, 0ull);
+        if (lo == elo && hi == ehi) break;
+    }
+}
+// Whether this piece completes the set; the count is then zero again.  The caller's
+// warp has synchronised; the fences order its partials before the count and the
+// merge's reads after it.
+__device__ __forceinline__ bool close_count(unsigned long long* ctr, int pieces) {
+    fence_acq_rel_gpu();
+    unsigned long long old;
+    asm volatile("atom.relaxed.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(ctr + 1) : "memory");
+    if (old + 1 != (unsigned long long)pieces) return false;
+    fence_acq_rel_gpu();
+    asm volatile("st.relaxed.gpu.global.u64 [%0], 0;" ::"l"(ctr + 1) : "memory");
+    return true;
+}
 __device__ __forceinline__ bool count_piece(unsigned long long* ctr, unsigned long long tag,
                                             int pieces) {
     unsigned long long lo = tag, hi = 0;           // a first guess: this call's, none counted
@@ -1550,10 +1622,54 @@ __device__ __forceinline__ void merge_slots(const float* part_o, const float* pa
     }
 }
 
-template <int R, int D, class Store>
+// WIDE (scored decode): all element passes of a few slots are in flight
+// together, so the loads' latency is paid once per few slots instead of once
+// per pass and pair of slots.
+template <int R, int D, bool WIDE = false, class Store>
 __device__ __forceinline__ void merge_cut(const float* part_o, const float* part_lse, int c0,
                                           int c1, int slot0, const float* x_o, const float* x_lse,
                                           int lane, Store&& store) {
+    if constexpr (WIDE) {
+        constexpr int EPL = merge_epl<R, D>(), NP = R * D / (32 * EPL);
+        constexpr int BATCH = 64 / (NP * EPL) > 8 ? 8 : (64 / (NP * EPL) < 1 ? 1 : 64 / (NP * EPL));
+        float M[NP], den[NP], acc[NP][EPL];
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            M[q] = -CUDART_INF_F;
+            den[q] = 0.f;
+#pragma unroll
+            for (int k = 0; k < EPL; ++k) acc[q][k] = 0.f;
+        }
+#pragma unroll 1
+        for (int c = c0; c <= c1; c += BATCH) {
+            float ls[BATCH][NP], ov[BATCH][NP][EPL];
+#pragma unroll
+            for (int t = 0; t < BATCH; ++t) {
+                const int cc = min(c + t, c1);         // (past the end: loaded, not added)
+                const size_t slot = (size_t)cc * 2 + (cc == c0 ? slot0 : 0);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    const int e0 = (q * 32 + lane) * EPL, r = e0 / D, d0 = e0 % D;
+                    ls[t][q] = __ldcg(part_lse + slot * R + r);
+                    load_row<EPL>(ov[t][q], part_o + (slot * R + r) * D + d0, true);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < BATCH; ++t)
+                if (c + t <= c1)
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) lse_add<EPL>(M[q], den[q], acc[q], ls[t][q], ov[t][q]);
+        }
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const int e0 = (q * 32 + lane) * EPL;
+            const float inv = den[q] > 0.f ? 1.f / den[q] : 0.f;
+#pragma unroll
+            for (int k = 0; k < EPL; ++k) acc[q][k] *= inv;
+            store(e0 / D, e0 % D, acc[q], den[q] > 0.f ? M[q] + fast_log2(den[q]) : -CUDART_INF_F);
+        }
+        return;
+    }
     merge_slots<R, D, kMergeBatch>(part_o, part_lse, c0, c1, slot0, x_o, x_lse, lane, 0, 1,
                                    static_cast<Store&&>(store));
 }
@@ -1682,7 +1798,8 @@ __device__ __forceinline__ int first_visible(const Params& p, int b, int L) {
     if (p.first != nullptr) lo = max(lo, p.first[b]);
     return min(lo, L);
 }
-template <bool MOD = false>
+// PER > 0: the sums of the sequences' pieces of PER units go into `pieces`.
+template <bool MOD = false, int PER = 0>
 __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem, const Layout& lay,
                                             int bsu, bool cascade, bool report) {
     const int B = p.batch, tid = threadIdx.x, nthreads = blockDim.x;
@@ -1698,7 +1815,7 @@ __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem
                             : 0;
     const int per = (B + nthreads - 1) / nthreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int local = 0;
+    int local = 0, local_p = 0;
     bool over = false;
     for (int b = b0; b < b1; ++b) {
         const int L = p.seq_lens[b];
@@ -1711,16 +1828,27 @@ __device__ __forceinline__ void unit_prefix(const Params& p, unsigned char* smem
         }
         if (cascade || MOD) skip_s[b] = skip;
         local += nb - skip;
+        if constexpr (MOD) local_p += (nb - skip + PER - 1) / PER;
     }
     if (over && report) atomicOr(p.err, KV_DEVERR_SEQ_RANGE);
     int total = 0;
     int run = block_excl_sum(local, warp_tot, &total);
+    int* pieces = reinterpret_cast<int*>(smem + lay.pieces);
+    int total_p = 0, run_p = 0;
+    if constexpr (MOD) run_p = block_excl_sum(local_p, warp_tot, &total_p);
     for (int b = b0; b < b1; ++b) {
         prefix[b] = run;
         const int nb = (min(max(p.seq_lens[b], 0), cap) + bsu - 1) / bsu;
         run += nb - (cascade || MOD ? skip_s[b] : 0);
+        if constexpr (MOD) {
+            pieces[b] = run_p;
+            run_p += (nb - skip_s[b] + PER - 1) / PER;
+        }
     }
-    if (tid == 0) prefix[B] = total;
+    if (tid == 0) {
+        prefix[B] = total;
+        if constexpr (MOD) pieces[B] = total_p;
+    }
 }
 
 // ------------------------------------------------------------ split kernel --
@@ -1768,7 +1896,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
     // reads the prefix states (and, at the latest, before each warp exits,
     // so that this grid never ends before the prefix pass).
     if (!cascade) pdl_wait();
-    unit_prefix<MOD>(p, smem, lay, bsu, cascade, blockIdx.x == 0);
+    unit_prefix<MOD, MOD ? Pol::kPer : 0>(p, smem, lay, bsu, cascade, blockIdx.x == 0);
     __syncthreads();
     // sequences no unit covers: zeros, or (cascade) the prefix state alone
     for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -1788,7 +1916,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
     // another of its CTA from here on.
     const int U = prefix[B] * H;
     const int worker = blockIdx.x * NCW + warp;
-    const WorkCut cut(prefix, B, H, p.num_ctas * NCW);
+    const auto cut = [&] {
+        if constexpr (MOD)
+            return ScoredCut(prefix, reinterpret_cast<const int*>(smem + lay.pieces), B, H,
+                             p.num_ctas * NCW, Pol::kPer);
+        else
+            return WorkCut(prefix, B, H, p.num_ctas * NCW);
+    }();
     const int start = cut.start_unit(worker);
     const int end = cut.start_unit(worker + 1);
     if (start >= end) {
@@ -1959,7 +2093,12 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
         }
 
         pol.begin(qbase + head0 * D, p.qscale, lane);
-        if constexpr (MOD) pol.set_mods(p, g * G, lane);
+        if constexpr (MOD) {
+            pol.set_mods(p, g * G, lane);
+            if (lane == 0 && p.merge_wpp == 0 && !(seg_start >= start && seg_start + nb <= end))
+                open_count(p.counters + 2 * ((size_t)b * H + g), p.tag);
+            __syncwarp();
+        }
 
         for (int uu = u; uu < piece_end; ++uu) {
             const int s = cs;
@@ -2012,17 +2151,20 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Pol::kMinBlocks) paged_decode_s
                 // Count the finished pieces of (b, g); the warp that finishes
                 // the last one merges all their partials into `out`.  (With
                 // merge_wpp > 0 the partials wait for paged_decode_merge.)
-                __threadfence();
+                if constexpr (!MOD) __threadfence();
                 __syncwarp();
                 const int c0 = cut.range_of(seg_start, b * H + g);
                 const int c1 = cut.range_of(seg_start + nb - 1, b * H + g);
                 int last = 0;
-                if (lane == 0)
-                    last = count_piece(p.counters + 2 * ((size_t)b * H + g), p.tag, c1 - c0 + 1);
+                if (lane == 0) {
+                    unsigned long long* ctr = p.counters + 2 * ((size_t)b * H + g);
+                    if constexpr (MOD) last = close_count(ctr, c1 - c0 + 1);
+                    else last = count_piece(ctr, p.tag, c1 - c0 + 1);
+                }
                 if (__shfl_sync(FULL, last, 0)) {
-                    __threadfence();
+                    if constexpr (!MOD) __threadfence();
                     T* ob = obase + head0 * D;
-                    merge_cut<G, D>(p.part_o, p.part_lse, c0, c1,
+                    merge_cut<G, D, MOD>(p.part_o, p.part_lse, c0, c1,
                                     seg_start == cut.start_unit(c0) ? 0 : 1, po.pst_o, po.pst_lse, lane,
                                     [&](int r, int d0, const float* v, float) {
 #pragma unroll
@@ -2100,7 +2242,7 @@ __device__ __forceinline__ void lse_range(const float* part_o, const float* part
 // shared memory (long contexts: dozens of partials per pair); merge_wpp = 1:
 // a warp per pair.  The split kernel's cut is recomputed here from the same
 // seq_lens and grid.
-template <typename T, int D, int G, int UB, bool MOD = false>
+template <typename T, int D, int G, int UB, bool MOD = false, int PER = 0>
 __global__ void __launch_bounds__(SPLIT_THREADS) paged_decode_merge(const Params p) {
     constexpr int EPL = merge_epl<G, D>();
     constexpr int NP = G * D / (32 * EPL);         // element passes of a warp
@@ -2114,9 +2256,15 @@ __global__ void __launch_bounds__(SPLIT_THREADS) paged_decode_merge(const Params
     float* red = reinterpret_cast<float*>(smem + lay.pst);   // [NCW][NP][32][EPL + 2]
     const bool cascade = !MOD && p.num_groups > 0;
     pdl_wait();                                    // the split kernel's partials are visible
-    unit_prefix<MOD>(p, smem, lay, bsu, cascade, false);
+    unit_prefix<MOD, PER>(p, smem, lay, bsu, cascade, false);
     __syncthreads();
-    const WorkCut cut(prefix, B, H, p.num_ctas * NCW);
+    const auto cut = [&] {
+        if constexpr (MOD)
+            return ScoredCut(prefix, reinterpret_cast<const int*>(smem + lay.pieces), B, H,
+                             p.num_ctas * NCW, PER);
+        else
+            return WorkCut(prefix, B, H, p.num_ctas * NCW);
+    }();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     T* obase = static_cast<T*>(p.out);
     auto store = [&](T* ob, int r, int d0, const float* v) {
@@ -2242,12 +2390,17 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     p.bs = pool.block_size;
     p.stages = plan.stages;
     // No more CTAs than ranges of kMinChunk units (the smallest range) that the
-    // tables can hold: fewer sequences cut exactly as on the full grid, without
-    // the CTAs that would find no work.
+    // tables can hold, or pieces: fewer sequences cut exactly as on the full grid,
+    // without the CTAs that would find no work.
     const int pairs = call.batch * pool.num_kv_heads;
-    const long long most = (long long)pairs * ((call.max_blocks + Pol::kUnitBlocks - 1) /
-                                               Pol::kUnitBlocks + kPieceCost);
-    const long long ranges = (most + kMinChunk - 1) / kMinChunk;
+    int most = (call.max_blocks + Pol::kUnitBlocks - 1) / Pol::kUnitBlocks;    // units of a (b, g)
+    long long ranges;
+    if constexpr (Pol::kMod) {
+        most = scored_units(*call.mods, most, pool.block_size * Pol::kUnitBlocks);
+        ranges = (long long)pairs * ((most + Pol::kPer - 1) / Pol::kPer);
+    } else {
+        ranges = ((long long)pairs * (most + kPieceCost) + kMinChunk - 1) / kMinChunk;
+    }
     p.num_ctas = (int)std::min<long long>(plan.num_ctas, (ranges + NCW - 1) / NCW);
     p.qscale = call.scale * 1.4426950408889634f;
     p.wait_ns = pool.wait_ns;
@@ -2278,7 +2431,7 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
     cfg.numAttrs = 1;
     // where the partials of cut (b, g) merge: in this kernel or a second one
     p.merge_wpp = merge_warps_per_pair(plan.num_ctas * NCW, pairs);
-    if (Pol::kMod && (long long)p.num_ctas * NCW * kMinChunk >= most && most <= kFewUnits * (long long)pairs)
+    if (Pol::kMod && ranges <= (long long)p.num_ctas * NCW && most <= kFewPieces * Pol::kPer)
         p.merge_wpp = 0;
     if (Pol::kH2)
         e = cudaLaunchKernelEx(&cfg, split, pool.tmap_k_h2, pool.tmap_v_h2, p);
@@ -2288,7 +2441,7 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
         e = cudaLaunchKernelEx(&cfg, split, pool.tmap_k, pool.tmap_v, p);
     if (e != cudaSuccess || p.merge_wpp == 0) return e;
     // the partials of (b, g) cut across warps, merged behind the split kernel
-    auto merge = paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod>;
+    auto merge = paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod, Pol::kMod ? Pol::kPer : 0>;
     const Layout ml(0, call.batch, pool.block_size * Pol::kUnitBlocks, G, D, 2, call.num_groups, 0, 0,
                     Pol::kMod);
     const size_t merge_smem = ml.pst + merge_red_bytes<G, D>() + 1024;
@@ -2296,7 +2449,8 @@ cudaError_t launch_typed(const kv_pool& pool, const DecodeCall& call, const Deco
                                                       pool.num_sms * 4)));
     cfg.dynamicSmemBytes = merge_smem;
     if (merge_smem > 48 * 1024) {
-        e = allow_smem<paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod>>(pool.device, merge_smem);
+        e = allow_smem<paged_decode_merge<T, D, G, Pol::kUnitBlocks, Pol::kMod, Pol::kMod ? Pol::kPer : 0>>(pool.device,
+                                                                                       merge_smem);
         if (e != cudaSuccess) return e;
     }
     return cudaLaunchKernelEx(&cfg, merge, p);

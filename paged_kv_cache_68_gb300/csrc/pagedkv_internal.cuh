@@ -62,13 +62,15 @@ struct kv_pool {
     int num_sms;
     // limit of one pipeline wait in the decode kernels (kv_pool_set_wait_limit)
     unsigned long long wait_ns = pagedkv::kWaitLimitNs;
-    // last decode plan, keyed by (batch, num_q_heads)
+    // the last decode plans (layers of several kinds take turns in one step)
+    struct PlanEntry {
+        int batch = -1, hq = -1, groups = -1;
+        bool scored = false, deep = false;
+        pagedkv::DecodePlan plan;
+    };
     std::mutex plan_mu;
-    int plan_batch = -1;
-    int plan_hq = -1;
-    int plan_groups = -1;
-    bool plan_scored = false;
-    pagedkv::DecodePlan plan;
+    PlanEntry plans[8];
+    int plan_next = 0;
 };
 
 namespace pagedkv {
@@ -204,7 +206,7 @@ struct DecodeCall {
 // (cached per pool).  Returns cudaErrorNotSupported for shapes with no
 // compiled kernel.
 cudaError_t plan_decode(kv_pool& pool, int batch, int num_q_heads, int num_groups, bool scored,
-                        DecodePlan* plan);
+                        DecodePlan* plan, bool deep = false);
 
 cudaError_t launch_decode(const kv_pool& pool, const DecodeCall& call, const DecodePlan& plan,
                           cudaStream_t stream);
