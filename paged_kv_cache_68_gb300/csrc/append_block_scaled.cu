@@ -30,7 +30,7 @@ namespace pagedkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kBigThreads = 512;          // many rows: 16 warps, a block's heads at once
 constexpr int kD = 128;
 constexpr int kMaxRows = 256;             // the largest block size
 constexpr int kHeld = 8;                  // row pairs a warp keeps in registers
@@ -39,9 +39,9 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 struct BlockAppend {
-    const uint4* fresh[2];                // the call's K and V rows
-    unsigned char* codes[2];
-    float* scales[2];
+    const uint4 *fresh_k, *fresh_v;       // the call's K and V rows
+    unsigned char *codes_k, *codes_v;
+    float *scales_k, *scales_v;
     const int64_t* slots;
     int* owner;
     int* leader;
@@ -58,14 +58,31 @@ template <> __device__ __forceinline__ float2 widen<__nv_bfloat16>(uint32_t w) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
-__device__ __forceinline__ uint32_t int8_code(float y) {
-    return (uint32_t)min(127, max(-127, __float2int_rn(y))) & 0xffu;
+// The bits above which a 16-bit value's magnitude is an infinity or NaN.
+template <typename T> constexpr uint32_t kInfBits = 0x7c00u;
+template <> constexpr uint32_t kInfBits<__nv_bfloat16> = 0x7f80u;
+
+// The INT8 code of y in the low byte: clamped to [-127, 127], then rounded to
+// nearest even by the addition of 1.5 * 2^23, whose sum holds the integer in its
+// low bits (an FMA-pipe step; a conversion instruction takes the MUFU's, at an
+// eighth of the rate).
+__device__ __forceinline__ uint32_t int8_bits(float y) {
+    return __float_as_uint(__fadd_rn(fminf(fmaxf(y, -127.f), 127.f), 12582912.f));
 }
 
 // Q of two values: the low 16 bits hold their codes.
 template <bool INT8> __device__ __forceinline__ uint32_t encode2(float a, float b) {
-    if constexpr (INT8) return int8_code(a) | (int8_code(b) << 8);
+    if constexpr (INT8) return __byte_perm(int8_bits(a), int8_bits(b), 0x0040) & 0xffffu;
     else return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Q of four, one word.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if constexpr (INT8)
+        return __byte_perm(__byte_perm(int8_bits(a), int8_bits(b), 0x0040),
+                           __byte_perm(int8_bits(c), int8_bits(d), 0x0040), 0x5410);
+    else
+        return encode2<false>(a, b) | (encode2<false>(c, d) << 16);
 }
 
 // Four codes, each rounded again after a factor.
@@ -84,8 +101,8 @@ template <bool INT8> __device__ __forceinline__ uint32_t rescale4(uint32_t w, fl
             v[2 * i + 1] = x.y;
         }
     }
-    return encode2<INT8>(__fmul_rn(v[0], f), __fmul_rn(v[1], f)) |
-           (encode2<INT8>(__fmul_rn(v[2], f), __fmul_rn(v[3], f)) << 16);
+    return encode4<INT8>(__fmul_rn(v[0], f), __fmul_rn(v[1], f), __fmul_rn(v[2], f),
+                         __fmul_rn(v[3], f));
 }
 
 __global__ void __launch_bounds__(kThreads) mark_rows_kernel(const BlockAppend p) {
@@ -111,46 +128,59 @@ __device__ __forceinline__ void quantise_head(const BlockAppend& p, int part, in
                                               const int* tok, const unsigned char* rows, int nw,
                                               int lane) {
     const int half = lane >> 4, hl = lane & 15;
-    float* scale = p.scales[part] + (size_t)blk * p.hkv + h;
+    float* scale = (part ? p.scales_v : p.scales_k) + (size_t)blk * p.hkv + h;
     const float old = tok[0] != 0 ? 0.f : *scale;
-    unsigned char* base = p.codes[part] + ((size_t)blk * p.bs * p.hkv + h) * kD;
-    const size_t row_bytes = (size_t)p.hkv * kD;
+    unsigned char* base = (part ? p.codes_v : p.codes_k) + ((size_t)blk * p.bs * p.hkv + h) * kD;
+    const uint4* fresh = (part ? p.fresh_v : p.fresh_k) + (size_t)h * (kD / 8) + hl;
+    const size_t row_bytes = (size_t)p.hkv * kD, fresh_row = (size_t)p.hkv * (kD / 8);
     uint4 w[kHeld];
     auto load = [&](int g) {
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int n = g + 2 * k + half;
             w[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (n < nw)
-                w[k] = __ldg(p.fresh[part] +
-                             ((size_t)(tok[rows[n]] - 1) * p.hkv + h) * (kD / 8) + hl);
+            if (n < nw) w[k] = __ldg(fresh + (size_t)(tok[rows[n]] - 1) * fresh_row);
         }
     };
-    float a = 0.f;
-    bool finite = true;
+    // The largest magnitude, as 16-bit patterns: without their sign they order as
+    // the values do, two to an instruction.
+    uint32_t top = 0u;
+#pragma unroll 1
     for (int g = 0; g < nw; g += 2 * kHeld) {
         load(g);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-            const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = widen<T>(ws[i]);
-                const bool fx = isfinite(f.x), fy = isfinite(f.y);
-                a = fmaxf(a, fmaxf(fx ? fabsf(f.x) : 0.f, fy ? fabsf(f.y) : 0.f));
-                finite = finite && fx && fy;
-            }
+            top = __vmaxu2(top, __vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu));
+            top = __vmaxu2(top, __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu));
         }
     }
+    top = max(top & 0xffffu, top >> 16);
+    top = __reduce_max_sync(kAll, top);
+    const bool finite = top < kInfBits<T>;
+    if (!finite) {                                   // the largest of the finite ones
+        top = 0u;
+        for (int g = 0; g < nw; g += 2 * kHeld) {
+            load(g);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
-    finite = __all_sync(kAll, finite);
+            for (int k = 0; k < kHeld; ++k) {
+                const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = ws[i] & 0x7fffu, hi = (ws[i] >> 16) & 0x7fffu;
+                    top = max(top, max(lo < kInfBits<T> ? lo : 0u, hi < kInfBits<T> ? hi : 0u));
+                }
+            }
+        }
+        top = __reduce_max_sync(kAll, top);
+    }
+    const float a = widen<T>(top).x;
     float now = fmaxf(old, __fdiv_rn(a, INT8 ? 127.f : 448.f));
     if (now < kTiny) now = 0.f;
     if (INT8 && (!finite || old != old)) now = __int_as_float(0x7fc00000);
     // the block's other rows, when the scale grew
     if (nw < p.bs && old > 0.f && now > old) {
         const float f = __fdiv_rn(old, now);
+#pragma unroll 1
         for (int r = lane >> 3; r < p.bs; r += 4)
             if (tok[r] == 0) {
                 uint4* c = reinterpret_cast<uint4*>(base + r * row_bytes) + (lane & 7);
@@ -163,86 +193,125 @@ __device__ __forceinline__ void quantise_head(const BlockAppend& p, int part, in
             }
     }
     const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;   // (0 for a NaN scale)
+#pragma unroll 1
     for (int g = 0; g < nw; g += 2 * kHeld) {
         if (nw > 2 * kHeld) load(g);                 // (else still held)
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int n = g + 2 * k + half;
-            const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-            uint32_t c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = widen<T>(ws[i]);
-                c[i] = encode2<INT8>(__fmul_rn(f.x, inv), __fmul_rn(f.y, inv));
-            }
+            const float2 i2 = make_float2(inv, inv);
+            const float2 f0 = __fmul2_rn(widen<T>(w[k].x), i2), f1 = __fmul2_rn(widen<T>(w[k].y), i2);
+            const float2 f2 = __fmul2_rn(widen<T>(w[k].z), i2), f3 = __fmul2_rn(widen<T>(w[k].w), i2);
+            const uint2 c = make_uint2(encode4<INT8>(f0.x, f0.y, f1.x, f1.y),
+                                       encode4<INT8>(f2.x, f2.y, f3.x, f3.y));
             if (n < nw)
                 *reinterpret_cast<uint2*>(base + rows[n] * row_bytes + hl * 8) =
-                    INT8 && now != now ? make_uint2(0u, 0u)
-                                       : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    INT8 && now != now ? make_uint2(0u, 0u) : c;
         }
     }
     if (lane == 0) *scale = now;
 }
 
-template <typename T, bool INT8, bool SCAN>
-__global__ void __launch_bounds__(kThreads) append_block_kernel(const BlockAppend p) {
+// The block's rows in `tok` (complete for every thread), by all warps of the CTA.
+template <typename T, bool INT8>
+__device__ __forceinline__ void quantise_block(const BlockAppend& p, int blk, const int* tok,
+                                               unsigned char* rows, int* nw_s) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        int n = 0;
+        for (int r0 = 0; r0 < p.bs; r0 += 32) {
+            const bool has = r0 + lane < p.bs && tok[r0 + lane] != 0;
+            const unsigned m = __ballot_sync(kAll, has);
+            if (has) rows[n + __popc(m & ((1u << lane) - 1u))] = (unsigned char)(r0 + lane);
+            n += __popc(m);
+        }
+        if (lane == 0) *nw_s = n;
+    }
+    __syncthreads();
+    const int nw = *nw_s;
+    for (int item = warp; item < 2 * p.hkv; item += (int)(blockDim.x >> 5))
+        quantise_head<T, INT8>(p, item & 1, item >> 1, blk, tok, rows, nw, lane);
+}
+
+// Up to kScanTokens rows: a CTA per token, which reads all slots itself.
+template <typename T, bool INT8>
+__global__ void __launch_bounds__(kThreads) append_scan_kernel(const BlockAppend p) {
     __shared__ int tok[kMaxRows];
     __shared__ unsigned char rows[kMaxRows];
     __shared__ int nw_s;
+    constexpr int kPer = kScanTokens / kThreads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int i0 = blockIdx.x * p.chunk, i1 = min(p.num_tokens, i0 + p.chunk);
-    for (int i = i0; i < i1; ++i) {                  // (every branch below is CTA-uniform)
+    const int tid = threadIdx.x, i = blockIdx.x;
+    const long long slot = p.slots[i];
+    long long others[kPer];                          // (in flight with the token's own)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int j = tid + k * kThreads;
+        others[k] = j < p.num_tokens ? p.slots[j] : -1;
+    }
+    if (tid < p.bs) tok[tid] = 0;
+    if (slot < 0) return;                            // padding
+    if (slot >= p.num_rows) {
+        if (tid == 0) atomicOr(p.err, KV_DEVERR_SLOT_RANGE);
+        return;
+    }
+    const int blk = (int)slot / p.bs;
+    const long long first = (long long)blk * p.bs;
+    __syncthreads();
+    bool later = false;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const long long r = others[k] - first;
+        if (others[k] >= 0 && r >= 0 && r < p.bs) {
+            const int j = tid + k * kThreads;
+            atomicMax(&tok[r], j + 1);
+            later = later || j > i;
+        }
+    }
+    if (__syncthreads_or(later)) return;             // a later token leads
+    quantise_block<T, INT8>(p, blk, tok, rows, &nw_s);
+}
+
+// Any number, after mark_rows_kernel: a CTA per `chunk` tokens writes the blocks
+// that they lead.  (The chunk's leaders are found at once: one token a thread.)
+template <typename T, bool INT8>
+__global__ void __launch_bounds__(kBigThreads, 2) append_marked_kernel(const BlockAppend p) {
+    __shared__ int tok[kMaxRows];
+    __shared__ unsigned char rows[kMaxRows];
+    __shared__ int led[kBigThreads];
+    __shared__ int nw_s, led_n;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x;
+    const int i = blockIdx.x * p.chunk + tid;
+    if (tid == 0) led_n = 0;
+    __syncthreads();
+    if (tid < p.chunk && i < p.num_tokens) {
         const long long slot = p.slots[i];
-        if (slot < 0) continue;                      // padding
-        if (slot >= p.num_rows) {
-            if (SCAN && tid == 0) atomicOr(p.err, KV_DEVERR_SLOT_RANGE);
-            continue;
+        if (slot >= 0 && slot < p.num_rows) {
+            const int blk = (int)slot / p.bs;
+            if (p.leader[blk] == i + 1) {
+                p.leader[blk] = 0;                   // (no other token equals it)
+                led[atomicAdd(&led_n, 1)] = blk;
+            }
         }
-        const int blk = (int)slot / p.bs;
-        if constexpr (SCAN) {
-            const long long first = (long long)blk * p.bs;
-            if (tid < p.bs) tok[tid] = 0;
-            __syncthreads();
-            bool later = false;
-            for (int j = tid; j < p.num_tokens; j += kThreads) {
-                const long long r = p.slots[j] - first;
-                if (r >= 0 && r < p.bs) {
-                    atomicMax(&tok[r], j + 1);
-                    later = later || j > i;
-                }
-            }
-            if (__syncthreads_or(later)) continue;   // a later token leads
-        } else {
-            if (p.leader[blk] != i + 1) continue;
-            if (tid < p.bs) {
-                tok[tid] = p.owner[(size_t)blk * p.bs + tid];
-                p.owner[(size_t)blk * p.bs + tid] = 0;
-            }
-            __syncthreads();                         // every thread has read the leader
-            if (tid == 0) p.leader[blk] = 0;
-        }
-        if (warp == 0) {
-            int n = 0;
-            for (int r0 = 0; r0 < p.bs; r0 += 32) {
-                const bool has = r0 + lane < p.bs && tok[r0 + lane] != 0;
-                const unsigned m = __ballot_sync(kAll, has);
-                if (has) rows[n + __popc(m & ((1u << lane) - 1u))] = (unsigned char)(r0 + lane);
-                n += __popc(m);
-            }
-            if (lane == 0) nw_s = n;
+    }
+    __syncthreads();
+    for (int k = 0; k < led_n; ++k) {
+        const int blk = led[k];
+        if (tid < p.bs) {
+            tok[tid] = p.owner[(size_t)blk * p.bs + tid];
+            p.owner[(size_t)blk * p.bs + tid] = 0;
         }
         __syncthreads();
-        const int nw = nw_s;
-        for (int item = warp; item < 2 * p.hkv; item += kWarps)
-            quantise_head<T, INT8>(p, item & 1, item >> 1, blk, tok, rows, nw, lane);
-        __syncthreads();                             // tok and rows before the next token's
+        quantise_block<T, INT8>(p, blk, tok, rows, &nw_s);
+        __syncthreads();                             // tok and rows before the next block's
     }
 }
 
 template <typename T, bool INT8>
-cudaError_t launch(const kv_pool& pool, const BlockAppend& call, cudaStream_t stream) {
+cudaError_t launch(const BlockAppend& call, cudaStream_t stream) {
     BlockAppend p = call;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -253,17 +322,18 @@ cudaError_t launch(const kv_pool& pool, const BlockAppend& call, cudaStream_t st
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (p.num_tokens <= kScanTokens) {
-        p.chunk = 1;
         cfg.gridDim = dim3((unsigned)p.num_tokens);
-        return cudaLaunchKernelEx(&cfg, append_block_kernel<T, INT8, true>, p);
+        return cudaLaunchKernelEx(&cfg, append_scan_kernel<T, INT8>, p);
     }
     cfg.gridDim = dim3((unsigned)((p.num_tokens + kThreads - 1) / kThreads));
     cudaError_t e = cudaLaunchKernelEx(&cfg, mark_rows_kernel, p);
     if (e != cudaSuccess) return e;
-    // about four CTAs' worth of tokens per SM: most tokens lead no block
-    p.chunk = std::max(1, p.num_tokens / (4 * pool.num_sms));
+    // as many tokens to a CTA as fill a block, when they come in order: then most
+    // CTAs lead one
+    p.chunk = std::min(p.bs, kBigThreads);
+    cfg.blockDim = dim3(kBigThreads);
     cfg.gridDim = dim3((unsigned)((p.num_tokens + p.chunk - 1) / p.chunk));
-    return cudaLaunchKernelEx(&cfg, append_block_kernel<T, INT8, false>, p);
+    return cudaLaunchKernelEx(&cfg, append_marked_kernel<T, INT8>, p);
 }
 
 }  // namespace
@@ -272,12 +342,12 @@ cudaError_t launch_append_block_scaled(const kv_pool& pool, const void* k_new, c
                                        const int64_t* slots, int num_tokens, cudaStream_t stream) {
     if (num_tokens <= 0) return cudaSuccess;
     BlockAppend p = {};
-    p.fresh[0] = static_cast<const uint4*>(k_new);
-    p.fresh[1] = static_cast<const uint4*>(v_new);
-    p.codes[0] = static_cast<unsigned char*>(pool.k);
-    p.codes[1] = static_cast<unsigned char*>(pool.v);
-    p.scales[0] = pool.k_scales;
-    p.scales[1] = pool.v_scales;
+    p.fresh_k = static_cast<const uint4*>(k_new);
+    p.fresh_v = static_cast<const uint4*>(v_new);
+    p.codes_k = static_cast<unsigned char*>(pool.k);
+    p.codes_v = static_cast<unsigned char*>(pool.v);
+    p.scales_k = pool.k_scales;
+    p.scales_v = pool.v_scales;
     p.slots = slots;
     p.owner = pool.d_owner;
     p.leader = pool.d_leader;
@@ -288,8 +358,8 @@ cudaError_t launch_append_block_scaled(const kv_pool& pool, const void* k_new, c
     p.hkv = pool.num_kv_heads;
     const bool bf = pool.dtype == KV_BF16;
     if (pool.cache_dtype == KV_INT8)
-        return bf ? launch<__nv_bfloat16, true>(pool, p, stream) : launch<__half, true>(pool, p, stream);
-    return bf ? launch<__nv_bfloat16, false>(pool, p, stream) : launch<__half, false>(pool, p, stream);
+        return bf ? launch<__nv_bfloat16, true>(p, stream) : launch<__half, true>(p, stream);
+    return bf ? launch<__nv_bfloat16, false>(p, stream) : launch<__half, false>(p, stream);
 }
 
 }  // namespace pagedkv

@@ -12,12 +12,17 @@ The module-level functions carry the C names (``kv_pool_create``,
 ``paged_attention_decode_cascade``, ``paged_attention_prefill``,
 ``paged_attention_decode_noalloc``,
 ``kv_pool_get_error``, ``kv_pool_clear_error``, ``kv_pool_destroy``);
-``KVPool`` bundles them for convenience.
+``KVPool`` bundles them for convenience; its ``plan_step``, ``decode_scored`` and
+``prefill_scored`` go through a small Python module over the same C ABI
+(``csrc/torch_binding.cpp``), which marshals their tensors without the
+interpreter time that ctypes costs beside a kernel of a few microseconds.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -112,6 +117,22 @@ def load(build: bool = True) -> ctypes.CDLL:
         return lib
 
 
+_binding = None
+
+
+def _fast():
+    """The compiled Python module (loaded with the library it calls)."""
+    global _binding
+    if _binding is None:
+        load()
+        loader = importlib.machinery.ExtensionFileLoader("_pagedkv_binding", _build.BINDING_PATH)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_pagedkv_binding", loader))
+        loader.exec_module(mod)
+        _binding = mod
+    return _binding
+
+
 def _check(status: int, what: str) -> None:
     if status != KV_OK:
         raise PagedKVError(status, what)
@@ -143,21 +164,9 @@ def _ptr(t: torch.Tensor, name: str, dtype, device: int) -> int:
     return t.data_ptr()
 
 
-def _opt(t, name: str, dtype, device: int):
-    return None if t is None else _ptr(t, name, dtype, device)
-
-
 def _shape(t, name: str, *shape) -> None:
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A result tensor, allocated on the stream that writes it."""
-    if isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
 
 
 # -- the C entry points, by name -----------------------------------------------
@@ -241,16 +250,27 @@ class StepPlan(NamedTuple):
     free_head: torch.Tensor       # int32 [1]
 
 
+def _plan_inputs(context_lens, new_lens, block_tables, free_blocks, free_head):
+    """The checked addresses and sizes of a step plan's inputs."""
+    dev, i32 = context_lens.get_device(), torch.int32
+    (b,) = context_lens.shape
+    _shape(new_lens, "new_lens", b)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError(f"block_tables must be [{b}, max_blocks]")
+    _shape(free_head, "free_head", 1)
+    return (_ptr(context_lens, "context_lens", i32, dev), _ptr(new_lens, "new_lens", i32, dev), b,
+            _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+            _ptr(free_blocks, "free_blocks", i32, dev), free_blocks.numel(),
+            _ptr(free_head, "free_head", i32, dev))
+
+
 def kv_plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free_head,
                  plan: StepPlan, stream=None) -> None:
     """context_lens, new_lens int32 [B]; block_tables int32 [B, max_blocks]
     (updated in place); free_blocks int32 [F], free_head int32 [1]; the results
     go into ``plan``."""
-    (b,), (t,) = context_lens.shape, plan.slot_mapping.shape
-    _shape(new_lens, "new_lens", b)
-    if block_tables.dim() != 2 or block_tables.shape[0] != b:
-        raise ValueError(f"block_tables must be [{b}, max_blocks]")
-    _shape(free_head, "free_head", 1)
+    args = _plan_inputs(context_lens, new_lens, block_tables, free_blocks, free_head)
+    b, (t,) = args[2], plan.slot_mapping.shape
     _shape(plan.free_head, "plan.free_head", 1)
     _shape(plan.cu_seqlens, "plan.cu_seqlens", b + 1)
     _shape(plan.seq_lens, "plan.seq_lens", b)
@@ -259,10 +279,7 @@ def kv_plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free
     if pos is not None:
         _shape(pos, "plan.positions", t)
     _check(load().kv_plan_step(
-        handle, _ptr(context_lens, "context_lens", i32, dev), _ptr(new_lens, "new_lens", i32, dev), b,
-        _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-        _ptr(free_blocks, "free_blocks", i32, dev), free_blocks.numel(),
-        _ptr(free_head, "free_head", i32, dev), _ptr(plan.free_head, "plan.free_head", i32, dev),
+        handle, *args, _ptr(plan.free_head, "plan.free_head", i32, dev),
         _ptr(plan.cu_seqlens, "plan.cu_seqlens", i32, dev),
         _ptr(plan.seq_lens, "plan.seq_lens", i32, dev),
         _ptr(plan.slot_mapping, "plan.slot_mapping", torch.int64, dev),
@@ -271,7 +288,7 @@ def kv_plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free
 
 
 def kv_append(handle, k_new, v_new, slot_mapping, dtype, stream=None) -> None:
-    t = int(slot_mapping.shape[0])
+    t = slot_mapping.shape[0]
     _check(load().kv_append(handle, _dev(k_new, "k_new", dtype), _dev(v_new, "v_new", dtype),
                             _dev(slot_mapping, "slot_mapping", torch.int64), t, _stream(stream)),
            "kv_append")
@@ -360,9 +377,11 @@ def paged_attention_decode_scored(handle, q, out, block_tables, seq_lens, scale:
     """``paged_attention_decode`` with tanh-capped scores (``softcap`` > 0), a
     bias -alibi_slopes[h] * distance (fp32 [Hq]), a ``window`` over the last
     positions and a first visible position per sequence (int32 [B])."""
-    b, hq, _ = q.shape
+    shape = q.shape
+    b, hq, _ = shape
     dev, i32 = q.get_device(), torch.int32
-    _shape(out, "out", *q.shape)
+    if out.shape != shape:
+        raise ValueError(f"out must be {list(shape)}, got {list(out.shape)}")
     _shape(seq_lens, "seq_lens", b)
     if block_tables.dim() != 2 or block_tables.shape[0] != b:
         raise ValueError(f"block_tables must be [{b}, max_blocks]")
@@ -371,8 +390,7 @@ def paged_attention_decode_scored(handle, q, out, block_tables, seq_lens, scale:
         handle, _ptr(q, "q", dtype, dev), _ptr(out, "out", dtype, dev),
         _ptr(block_tables, "block_tables", i32, dev), block_tables.shape[1],
         _ptr(seq_lens, "seq_lens", i32, dev), b, hq, scale, num_kv_heads, ctypes.byref(mods),
-        _ptr(workspace, "workspace", workspace.dtype, dev),
-        workspace.numel() * workspace.element_size(), _stream(stream)),
+        _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes, _stream(stream)),
         "paged_attention_decode_scored")
 
 
@@ -491,6 +509,7 @@ class KVPool:
             self.dtype = dtype
             self.handle = kv_pool_create_quantized(k_pool, v_pool, dtype, cache, k_scales,
                                                    v_scales, k_scale, v_scale)
+        self._h = self.handle.value
         self._ws: Optional[torch.Tensor] = None
         self._scored_need = {}                  # workspace bytes by (batch, query heads)
 
@@ -498,6 +517,7 @@ class KVPool:
         if self.handle is not None:
             kv_pool_destroy(self.handle)
             self.handle = None
+            self._h = 0
 
     def __del__(self):
         try:
@@ -509,17 +529,21 @@ class KVPool:
                   num_tokens: int, out: Optional[StepPlan] = None, stream=None) -> StepPlan:
         """Block tables (in place), slots, positions, offsets and lengths of one
         step, built on the GPU; ``num_tokens`` sizes the token arrays."""
-        if out is None:
-            dev, b = context_lens.device, context_lens.numel()
-            # one allocation for the int32 results
-            i32 = _new(num_tokens + 2 * b + 2, torch.int32, dev, stream)
-            pos, cu, lens, head = i32.split((num_tokens, b + 1, b, 1))
-            out = StepPlan(cu, lens, _new(num_tokens, torch.int64, dev, stream), pos, head)
-        elif out.slot_mapping.numel() != num_tokens:
-            raise ValueError(f"out.slot_mapping must hold {num_tokens} tokens")
-        kv_plan_step(self.handle, context_lens, new_lens, block_tables, free_blocks, free_head, out,
-                     stream)
-        return out
+        if out is not None:
+            if out.slot_mapping.numel() != num_tokens:
+                raise ValueError(f"out.slot_mapping must hold {num_tokens} tokens")
+            kv_plan_step(self.handle, context_lens, new_lens, block_tables, free_blocks, free_head,
+                         out, stream)
+            return out
+        if isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                return self.plan_step(context_lens, new_lens, block_tables, free_blocks, free_head,
+                                      num_tokens)
+        r = _fast().plan_step(self._h, context_lens, new_lens, block_tables, free_blocks, free_head,
+                              num_tokens, stream)
+        if type(r) is int:
+            raise PagedKVError(r, "kv_plan_step")
+        return StepPlan._make(r)
 
     def append(self, k_new, v_new, slot_mapping, stream=None) -> None:
         kv_append(self.handle, k_new, v_new, slot_mapping, self.dtype, stream)
@@ -580,15 +604,23 @@ class KVPool:
                       workspace=None, stream=None) -> torch.Tensor:
         """Decode with capped or biased scores and masks
         (``paged_attention_decode_scored``)."""
-        if out is None:
-            out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
+        if isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                return self.decode_scored(q, block_tables, seq_lens, scale, softcap=softcap,
+                                          alibi_slopes=alibi_slopes, window=window,
+                                          first_visible=first_visible, out=out, workspace=workspace)
+        self._own_type(q)
         if workspace is None:
             workspace = self.scored_workspace(q.shape[0], q.shape[1])
-        paged_attention_decode_scored(self.handle, q, out, block_tables, seq_lens, scale,
-                                      self.num_kv_heads, workspace, self.dtype, softcap=softcap,
-                                      alibi_slopes=alibi_slopes, window=window,
-                                      first_visible=first_visible, stream=stream)
-        return out
+        r = _fast().decode_scored(self._h, q, block_tables, seq_lens, scale, self.num_kv_heads, softcap,
+                                  alibi_slopes, window, first_visible, out, workspace, stream)
+        if type(r) is int:
+            raise PagedKVError(r, "paged_attention_decode_scored")
+        return r
+
+    def _own_type(self, q) -> None:
+        if q.dtype != self.dtype or q.dim() != 3:
+            raise ValueError(f"q must be a 3-D {self.dtype} tensor, got {q.dim()}-D {q.dtype}")
 
     def decode_cascade(self, q, block_tables, seq_lens, scale: float, groups, out=None,
                        workspace=None, stream=None) -> torch.Tensor:
@@ -623,14 +655,18 @@ class KVPool:
                        first_visible=None, prefix_lens=None, out=None, stream=None) -> torch.Tensor:
         """Chunked prefill with capped or biased scores and masks
         (``paged_attention_prefill_scored``)."""
-        if out is None:
-            out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
-        paged_attention_prefill_scored(self.handle, q, out, cu_seqlens, max_query_len,
-                                       block_tables, seq_lens, scale, self.num_kv_heads,
-                                       self.dtype, softcap=softcap, alibi_slopes=alibi_slopes,
-                                       window=window, first_visible=first_visible,
-                                       prefix_lens=prefix_lens, stream=stream)
-        return out
+        if isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                return self.prefill_scored(q, cu_seqlens, max_query_len, block_tables, seq_lens, scale,
+                                           softcap=softcap, alibi_slopes=alibi_slopes, window=window,
+                                           first_visible=first_visible, prefix_lens=prefix_lens, out=out)
+        self._own_type(q)
+        r = _fast().prefill_scored(self._h, q, cu_seqlens, max_query_len, block_tables, seq_lens,
+                                   scale, self.num_kv_heads, softcap, alibi_slopes, window,
+                                   first_visible, prefix_lens, out, stream)
+        if type(r) is int:
+            raise PagedKVError(r, "paged_attention_prefill_scored")
+        return r
 
     def set_wait_limit(self, limit_ns: int) -> None:
         kv_pool_set_wait_limit(self.handle, limit_ns)

@@ -134,3 +134,29 @@ def test_score_mods_layout_matches_the_header(tmp_path):
     got = list(map(int, subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()))
     want = [getattr(pagedkv.ScoreMods, n).offset for n in names] + [ctypes.sizeof(pagedkv.ScoreMods)]
     assert got == want
+
+
+def test_the_python_module_refuses_wrong_tensors():
+    """Shapes, counts and host tensors are refused before any call."""
+    from paged_kv_cache_68_gb300 import pagedkv
+    m = pagedkv._fast()
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    plan = [0, i(3), i(3), i(3, 4), i(9), i(1), 5, None]
+    with pytest.raises(TypeError):
+        m.plan_step(*plan[:-1])
+    for k, bad in ((1, 7), (1, i(3, 1)), (2, i(2)), (3, i(3)), (3, i(2, 4)), (5, i(2)), (6, -1),
+                   (6, 1 << 40), (1, i(3))):
+        with pytest.raises(ValueError):
+            m.plan_step(*[bad if n == k else a for n, a in enumerate(plan)])
+    q = torch.zeros(2, 4, 128)
+    dec = [0, q, i(2, 3), i(2), 0.1, 2, 0.0, None, 0, None, None, i(1), None]
+    pre = [0, q, i(3), 1, i(2, 3), i(2), 0.1, 2, 0.0, None, 0, None, None, None, None]
+    for fn, good, bads in ((m.decode_scored, dec, ((1, q[0]), (2, i(3, 3)), (3, i(3)), (7, i(4)),
+                                                   (9, i(3)), (8, 1 << 40))),
+                           (m.prefill_scored, pre, ((1, q[0]), (2, i(2)), (4, i(2)), (9, i(4)),
+                                                    (11, i(3)), (12, i(1))))):
+        with pytest.raises(TypeError):
+            fn(*good[1:])
+        for k, bad in bads + ((1, q),):
+            with pytest.raises(ValueError):
+                fn(*[bad if n == k else a for n, a in enumerate(good)])
