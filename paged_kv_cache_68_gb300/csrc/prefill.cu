@@ -12,6 +12,8 @@ cudaError_t prefill_block_f16(const kv_pool&, const PrefillCall&, cudaStream_t);
 cudaError_t prefill_block_bf16(const kv_pool&, const PrefillCall&, cudaStream_t);
 cudaError_t prefill_scored_f16(const kv_pool&, const PrefillCall&, cudaStream_t);
 cudaError_t prefill_scored_bf16(const kv_pool&, const PrefillCall&, cudaStream_t);
+cudaError_t prefill_scored_q8_f16(const kv_pool&, const PrefillCall&, cudaStream_t);
+cudaError_t prefill_scored_q8_bf16(const kv_pool&, const PrefillCall&, cudaStream_t);
 cudaError_t prefill_scored_block_f16(const kv_pool&, const PrefillCall&, cudaStream_t);
 cudaError_t prefill_scored_block_bf16(const kv_pool&, const PrefillCall&, cudaStream_t);
 
@@ -22,6 +24,8 @@ cudaError_t launch_prefill(const kv_pool& pool, const PrefillCall& c, cudaStream
         if (c.mods) return (bf ? prefill_scored_block_bf16 : prefill_scored_block_f16)(pool, c, stream);
         return (bf ? prefill_block_bf16 : prefill_block_f16)(pool, c, stream);
     }
+    if (c.mods && is_q8(pool))
+        return (bf ? prefill_scored_q8_bf16 : prefill_scored_q8_f16)(pool, c, stream);
     if (c.mods) return (bf ? prefill_scored_bf16 : prefill_scored_f16)(pool, c, stream);
     return (bf ? prefill_bf16 : prefill_f16)(pool, c, stream);
 }

@@ -4,7 +4,8 @@
 namespace pagedkv {
 
 cudaError_t prefill_bf16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    return pf::launch_format<__nv_bfloat16, false>(pool, c, stream);
+    using namespace pf;
+    return launch_plain<__nv_bfloat16>(pool, c, stream);
 }
 
 }  // namespace pagedkv

@@ -4,7 +4,8 @@
 namespace pagedkv {
 
 cudaError_t prefill_block_bf16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    return pf::launch_block<__nv_bfloat16, false>(pool, c, stream);
+    using namespace pf;
+    return launch_block<__nv_bfloat16, 0>(pool, c, stream);
 }
 
 }  // namespace pagedkv

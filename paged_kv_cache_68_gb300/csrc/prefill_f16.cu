@@ -4,7 +4,8 @@
 namespace pagedkv {
 
 cudaError_t prefill_f16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    return pf::launch_format<__half, false>(pool, c, stream);
+    using namespace pf;
+    return launch_plain<__half>(pool, c, stream);
 }
 
 }  // namespace pagedkv

@@ -378,6 +378,14 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
     return false;
 }
 
+// Scored prefill's kinds (MODS; 0: plain): what the loop over the tiles holds code
+// for.  16-bit pools have a kernel for masks alone and with a cap, a bias or both:
+// code that a call does not run still costs its instruction fetches (adding a
+// second form of the cap to one kernel for all slowed calls without a cap by 8 %).
+// On 8-bit pools, where the conversion of the codes bounds more, one kernel
+// decides as it runs.
+constexpr int kModsMask = 1, kModsCap = 2, kModsBias = 4, kModsAny = 8;
+
 // FMT: -1 for 16-bit pools (of type T), else the 8-bit pool's code format
 // (T is then the queries' type); the K / V maps address code rows.  SC: where
 // an 8-bit pool's scales are; a block's scale is read once for each of its
@@ -390,7 +398,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
 // first to the last position that any of the CTA's queries sees; each row
 // masks what lies outside its own lo..hi.
 template <typename T, int G, int FMT = -1,
-          int SC = FMT == dec::kFmtInt8 ? dec::kScToken : dec::kScPool, bool MOD = false>
+          int SC = FMT == dec::kFmtInt8 ? dec::kScToken : dec::kScPool, int MODS = 0>
 __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     paged_prefill(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_k,
@@ -398,6 +406,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     constexpr bool Q8 = FMT >= 0;
     constexpr bool SCALES = Q8 && SC != dec::kScPool;
     constexpr bool BLOCKSC = Q8 && SC == dec::kScBlock;
+    constexpr bool MOD = MODS != 0, ANY = (MODS & kModsAny) != 0;
     // 8-bit pools: the products run on f16 (bf16 queries are converted)
     using MT = typename std::conditional<Q8, __half, T>::type;
     constexpr bool QCONV = Q8 && !std::is_same<T, __half>::value;
@@ -801,7 +810,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
         float slope2 = 0.f;                        // the head's slope, base 2
         if constexpr (MOD) {
             if (valid) visible_range(p, pos, L, prefix, cu0 + q0 + x * QT + qi, lo, lim);
-            if (p.slopes != nullptr) slope2 = p.slopes[g * G + hh] * 1.4426950408889634f;
+            if (ANY ? p.slopes != nullptr : (MODS & kModsBias) != 0) slope2 = p.slopes[g * G + hh] * 1.4426950408889634f;
         }
         const uint32_t trow = tmem + (uint32_t)x * COL_STREAM + ((uint32_t)(32 * qd) << 16);
         const int stid = tid - x * NSOFT * 32;     // thread index within the stream
@@ -902,51 +911,73 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                         sv[c][e] = __float_as_uint(__uint_as_float(sv[c][e]) *
                                                    (BLOCKSC ? kf[2 * c + e / 16] : tsc[32 * c + e]));
             }
+            // MOD: sv becomes what the score is sv * sq + off of, in base 2.
+            float sq = MOD ? 1.f : qs, off = 0.f;
             if constexpr (MOD) {
                 // (acc -> base-2 score, for the row's 16-token groups)
                 auto q2 = [&](int c, int e) {
                     const float f = BLOCKSC ? row_qs * kf[2 * c + e / 16] : row_qs;
                     return make_float2(f, f);
                 };
-                if (p.softcap > 0.f) {
-                    const float cap2 = p.softcap * 1.4426950408889634f;
+                auto pair = [&](int c, int e) {
+                    return make_float2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+                };
+                auto put = [&](int c, int e, float2 y) {
+                    sv[c][e] = __float_as_uint(y.x);
+                    sv[c][e + 1] = __float_as_uint(y.y);
+                };
+                constexpr bool kBias = ANY || (MODS & kModsBias) != 0;
+                if (ANY ? p.softcap > 0.f : (MODS & kModsCap) != 0) {
+                    // cap tanh(s / cap) = cap - 2 cap / (1 + exp(2 s / cap)): sv = -1 / (1 +
+                    // exp(...)), rising with the score, and the rest is the softmax's
+                    // own multiply-add
                     const float2 i2 = make_float2(2.f * p.inv_softcap, 2.f * p.inv_softcap);
-                    const float2 c2 = make_float2(cap2, cap2), n2 = make_float2(-2.f * cap2, -2.f * cap2);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][e]),
-                                                                    __uint_as_float(sv[c][e + 1])),
-                                                        __fmul2_rn(q2(c, e), i2));
+                            const float2 y = __fmul2_rn(pair(c, e), __fmul2_rn(q2(c, e), i2));
                             const float2 d = __fadd2_rn(
-                                make_float2(dec::fast_exp2(y.x), dec::fast_exp2(y.y)),
-                                make_float2(1.f, 1.f));
-                            const float2 s2 = __ffma2_rn(
-                                n2, make_float2(dec::fast_rcp(d.x), dec::fast_rcp(d.y)), c2);
-                            sv[c][e] = __float_as_uint(s2.x);
-                            sv[c][e + 1] = __float_as_uint(s2.y);
+                                make_float2(-dec::fast_exp2(y.x), -dec::fast_exp2(y.y)),
+                                make_float2(-1.f, -1.f));
+                            put(c, e, make_float2(dec::fast_rcp(d.x), dec::fast_rcp(d.y)));
                         }
+                    off = p.softcap * 1.4426950408889634f;
+                    sq = 2.f * off;
+                } else if constexpr (BLOCKSC) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) put(c, e, __fmul2_rn(pair(c, e), q2(c, e)));
                 } else {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(sv[c][e]),
-                                                                    __uint_as_float(sv[c][e + 1])),
-                                                        q2(c, e));
-                            sv[c][e] = __float_as_uint(y.x);
-                            sv[c][e + 1] = __float_as_uint(y.y);
-                        }
+                    sq = row_qs;
                 }
-                if (p.slopes != nullptr) {
-                    const float d0 = (float)(t0 - pos);
+                if (kBias && (ANY ? p.slopes != nullptr : true)) {
+                    // s - slope |P - t|.  On tiles past which no row of the warp sees,
+                    // |P - t| = P - t: the tile's constant part goes into `off`.
+                    if (prefix == 0 || __all_sync(FULL, t0 + BN - 1 <= pos)) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            sv[c][e] = __float_as_uint(fmaf(-slope2, fabsf(d0 + (float)(32 * c + e)),
-                                                            __uint_as_float(sv[c][e])));
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 y = __fmul2_rn(pair(c, e), make_float2(sq, sq));
+                                put(c, e, make_float2(fmaf(slope2, (float)(32 * c + e), y.x),
+                                                      fmaf(slope2, (float)(32 * c + e + 1), y.y)));
+                            }
+                        off += slope2 * (float)(t0 - pos);
+                    } else {
+                        const float d0 = (float)(t0 - pos);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 y = __fmul2_rn(pair(c, e), make_float2(sq, sq));
+                                put(c, e,
+                                    make_float2(fmaf(-slope2, fabsf(d0 + (float)(32 * c + e)), y.x),
+                                                fmaf(-slope2, fabsf(d0 + (float)(32 * c + e + 1)), y.y)));
+                            }
+                    }
+                    sq = 1.f;
                 }
                 if (t0 < lo) {
 #pragma unroll
@@ -972,7 +1003,8 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 for (int e = 2; e < 32; e += 2)
                     mx2[c] = max3(mx2[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
             }
-            const float m_new = fmaxf(m, MOD ? fmaxf(mx2[0], mx2[1]) : fmaxf(mx2[0], mx2[1]) * qs);
+            const float m_new = fmaxf(m, MOD ? fmaf(fmaxf(mx2[0], mx2[1]), sq, off)
+                                             : fmaxf(mx2[0], mx2[1]) * qs);
             float alpha = 1.f;
             const bool grow = m_new > m + kRescaleLog2;   // false while both are -inf
             if (grow) {
@@ -984,7 +1016,8 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             l2[1] = __fmul2_rn(l2[1], make_float2(alpha, alpha));
             // P = hi + lo of the tile's 64 tokens, in registers until PV_{j-1}
             // has finished with the P columns
-            const float2 qs2 = make_float2(qs, qs), nmu2 = make_float2(-mu, -mu);
+            const float nmu = MOD ? off - mu : -mu;
+            const float2 qs2 = make_float2(sq, sq), nmu2 = make_float2(nmu, nmu);
             uint32_t ph[32], pl[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -992,7 +1025,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 for (int e = 0; e < 32; e += 2) {
                     const float2 sc2 =
                         make_float2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
-                    const float2 xx = MOD ? __fadd2_rn(sc2, nmu2) : __ffma2_rn(sc2, qs2, nmu2);
+                    const float2 xx = __ffma2_rn(sc2, qs2, nmu2);
                     const float2 pp = make_float2(dec::fast_exp2(xx.x), dec::fast_exp2(xx.y));
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], pp);
                     float2 pv = pp;

@@ -11,8 +11,8 @@ namespace pagedkv {
 namespace pf {
 
 // FMT: -1 for 16-bit pools, else the 8-bit pool's code format; SC: its kind of
-// scales; MOD: scored prefill.
-template <typename T, int G, int FMT, int SC, bool MOD>
+// scales; MODS: scored prefill's kind.
+template <typename T, int G, int FMT, int SC, int MODS>
 cudaError_t launch_typed(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
     constexpr bool Q8 = FMT >= 0;
     constexpr int QT = BM / G;
@@ -45,9 +45,9 @@ cudaError_t launch_typed(const kv_pool& pool, const PrefillCall& c, cudaStream_t
         mk = &tk;
         mv = &tv;
     }
-    auto kern = paged_prefill<T, G, FMT, SC, MOD>;
+    auto kern = paged_prefill<T, G, FMT, SC, MODS>;
     constexpr uint32_t smem_bytes = Lay<Q8>::bytes;
-    cudaError_t e = dec::allow_smem<paged_prefill<T, G, FMT, SC, MOD>>(pool.device, smem_bytes);
+    cudaError_t e = dec::allow_smem<paged_prefill<T, G, FMT, SC, MODS>>(pool.device, smem_bytes);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = c.q;
@@ -93,35 +93,49 @@ cudaError_t launch_typed(const kv_pool& pool, const PrefillCall& c, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kern, tmap_q, *mk, *mv, p);
 }
 
-template <typename T, int FMT, int SC, bool MOD>
+template <typename T, int FMT, int SC, int MODS>
 cudaError_t launch_group(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
     switch (c.num_q_heads / pool.num_kv_heads) {
-        case 1: return launch_typed<T, 1, FMT, SC, MOD>(pool, c, stream);
-        case 2: return launch_typed<T, 2, FMT, SC, MOD>(pool, c, stream);
-        case 4: return launch_typed<T, 4, FMT, SC, MOD>(pool, c, stream);
-        case 8: return launch_typed<T, 8, FMT, SC, MOD>(pool, c, stream);
+        case 1: return launch_typed<T, 1, FMT, SC, MODS>(pool, c, stream);
+        case 2: return launch_typed<T, 2, FMT, SC, MODS>(pool, c, stream);
+        case 4: return launch_typed<T, 4, FMT, SC, MODS>(pool, c, stream);
+        case 8: return launch_typed<T, 8, FMT, SC, MODS>(pool, c, stream);
     }
     return cudaErrorNotSupported;
 }
 
-// 16-bit pools, and 8-bit pools with pool or token scales.
-template <typename T, bool MOD>
-cudaError_t launch_format(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    if (pool.block_scales) return cudaErrorNotSupported;
+// 8-bit pools with pool or token scales; MODS: 0 or kModsAny.
+template <typename T, int MODS>
+cudaError_t launch_q8(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
     if (pool.cache_dtype == KV_FP8_E4M3)
-        return launch_group<T, dec::kFmtE4M3, dec::kScPool, MOD>(pool, c, stream);
-    if (pool.cache_dtype == KV_INT8)
-        return launch_group<T, dec::kFmtInt8, dec::kScToken, MOD>(pool, c, stream);
-    return launch_group<T, -1, dec::kScPool, MOD>(pool, c, stream);
+        return launch_group<T, dec::kFmtE4M3, dec::kScPool, MODS>(pool, c, stream);
+    return launch_group<T, dec::kFmtInt8, dec::kScToken, MODS>(pool, c, stream);
 }
 
 // Block-scaled pools.
-template <typename T, bool MOD>
+template <typename T, int MODS>
 cudaError_t launch_block(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    if (!pool.block_scales) return cudaErrorNotSupported;
     if (pool.cache_dtype == KV_FP8_E4M3)
-        return launch_group<T, dec::kFmtE4M3, dec::kScBlock, MOD>(pool, c, stream);
-    return launch_group<T, dec::kFmtInt8, dec::kScBlock, MOD>(pool, c, stream);
+        return launch_group<T, dec::kFmtE4M3, dec::kScBlock, MODS>(pool, c, stream);
+    return launch_group<T, dec::kFmtInt8, dec::kScBlock, MODS>(pool, c, stream);
+}
+
+// Plain prefill of 16-bit and 8-bit pools.
+template <typename T>
+cudaError_t launch_plain(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
+    if (is_q8(pool)) return launch_q8<T, 0>(pool, c, stream);
+    return launch_group<T, -1, dec::kScPool, 0>(pool, c, stream);
+}
+
+// Scored prefill of 16-bit pools: the kernel of the call's kind.
+template <typename T>
+cudaError_t launch_scored(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
+    constexpr int m = kModsMask, sc = dec::kScPool;
+    const bool cap = c.mods->softcap > 0.f, bias = c.mods->alibi_slopes != nullptr;
+    if (cap && bias) return launch_group<T, -1, sc, m | kModsCap | kModsBias>(pool, c, stream);
+    if (cap) return launch_group<T, -1, sc, m | kModsCap>(pool, c, stream);
+    if (bias) return launch_group<T, -1, sc, m | kModsBias>(pool, c, stream);
+    return launch_group<T, -1, sc, m>(pool, c, stream);
 }
 
 }  // namespace pf

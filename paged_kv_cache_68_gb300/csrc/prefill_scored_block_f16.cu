@@ -4,7 +4,8 @@
 namespace pagedkv {
 
 cudaError_t prefill_scored_block_f16(const kv_pool& pool, const PrefillCall& c, cudaStream_t stream) {
-    return pf::launch_block<__half, true>(pool, c, stream);
+    using namespace pf;
+    return launch_block<__half, kModsAny>(pool, c, stream);
 }
 
 }  // namespace pagedkv
