@@ -165,10 +165,11 @@ kv_status kv_pool_create_quantized(int num_blocks, int block_size, int num_kv_he
  *     a = max |x| over the rows; old = the stored scale, or 0 when row 0 is one
  *     of the rows (the block starts anew);
  *     new = max(old, a / qmax), and 0 if that is below 2^-126;
- *     a row written: code = Q(x * (1 / new)) (0 when new is 0);
+ *     a row written: code = Q(x * (1 / new)), 1 / new taken as 0 when new is 0;
  *     a row not written, if new > old > 0: code = Q(code * (old / new)).
  *   Q rounds to nearest even and saturates (448, 127).  FP8: infinities and
- *   NaN do not count in a; an infinity saturates and NaN stays NaN.  INT8: a
+ *   NaN do not count in a; an infinity saturates (in a block whose finite
+ *   values are all 0 it becomes NaN) and NaN stays NaN.  INT8: a
  *   row holding either gives the block and head the scale NaN, with codes 0 for
  *   the call's rows, until the block starts anew.
  *   The first write to a block must therefore include its row 0 (as appending
@@ -369,7 +370,7 @@ kv_status paged_attention_decode(kv_pool_t pool, const void* q, void* out,
  *                                                     position of its document)
  * A query that sees nothing gives zeros.
  *
- * softcap: >= 0, finite; 0 = none.  window: >= 0; 0 = none.
+ * softcap: 0 = none, else 2^-10 to 2^10.  window: >= 0; 0 = none.
  * alibi_slopes: device fp32 [num_q_heads], finite, or NULL.
  * first_visible: device int32, decode [batch], prefill [num_tokens], or NULL;
  *   values below 0 count as 0.

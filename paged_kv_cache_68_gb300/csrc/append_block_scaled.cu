@@ -108,8 +108,9 @@ template <bool INT8> __device__ __forceinline__ uint32_t rescale4(uint32_t w, fl
 __global__ void __launch_bounds__(kThreads) mark_rows_kernel(const BlockAppend p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= p.num_tokens) return;
+    const long long ii = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (ii >= p.num_tokens) return;
+    const int i = (int)ii;
     const long long slot = p.slots[i];
     if (slot < 0) return;
     if (slot >= p.num_rows) {
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kBigThreads, 2) append_marked_kernel(const Blo
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
-    const int i = blockIdx.x * p.chunk + tid;
+    const long long i = (long long)blockIdx.x * p.chunk + tid;
     if (tid == 0) led_n = 0;
     __syncthreads();
     if (tid < p.chunk && i < p.num_tokens) {

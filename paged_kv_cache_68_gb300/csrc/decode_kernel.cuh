@@ -77,7 +77,7 @@ constexpr int kPerUnits = 4, kPerLargeUnits = 2;
 // The most units of `bsu` tokens that a sequence of at most `units` can see: a
 // window of w tokens touches (w - 1) / bsu + 2 of them at most.
 inline int scored_units(const kv_score_mods& mods, int units, int bsu) {
-    return mods.window > 0 ? std::min(units, (mods.window - 1) / bsu + 2) : units;
+    return mods.window > 0 ? (int)std::min<long long>(units, (mods.window - 1ll) / bsu + 2) : units;
 }
 
 struct Params {
@@ -500,7 +500,7 @@ template <> struct TReduce<1, 0> {
 };
 
 // Largest b in [0, B) with prefix[b] * H <= u (prefix[0] = 0 <= u < prefix[B] * H).
-__device__ __forceinline__ int find_seq(const int* prefix, int B, int u, int H) {
+__host__ __device__ __forceinline__ int find_seq(const int* prefix, int B, int u, int H) {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -564,15 +564,15 @@ struct ScoredCut {
     const int* pieces;     // [B + 1] pieces of KV head 0 before each sequence
     int per;
     bool aligned;
-    __device__ __forceinline__ ScoredCut(const int* pre, const int* pcs, int B, int H, int W, int per_)
+    __host__ __device__ __forceinline__ ScoredCut(const int* pre, const int* pcs, int B, int H, int W, int per_)
         : cut(pre, B, H, W), pieces(pcs), per(per_), aligned(pcs[B] * H <= W) {}
-    __device__ __forceinline__ int range_of(int u, int s) const {
+    __host__ __device__ __forceinline__ int range_of(int u, int s) const {
         if (!aligned) return cut.range_of(u, s);
         const int H = cut.H, b = s / H, g = s - b * H;
         const int seg = cut.prefix[b] * H + g * (cut.prefix[b + 1] - cut.prefix[b]);
         return pieces[b] * H + g * (pieces[b + 1] - pieces[b]) + (u - seg) / per;
     }
-    __device__ __forceinline__ int start_unit(int c) const {
+    __host__ __device__ __forceinline__ int start_unit(int c) const {
         if (!aligned) return cut.start_unit(c);
         const int H = cut.H, B = cut.B;
         if (c >= pieces[B] * H) return cut.prefix[B] * H;

@@ -236,9 +236,14 @@ PKV_DECODE_UNIT(scored_q8_f16) PKV_DECODE_UNIT(scored_q8_bf16)
 PKV_DECODE_UNIT(scored_block_f16) PKV_DECODE_UNIT(scored_block_bf16)
 #undef PKV_DECODE_UNIT
 
+// A cap's range: cap tanh(s / cap) is taken as cap - 2 cap / (1 + exp(2 s / cap)),
+// whose absolute error is about cap 2^-22 (2.4e-4 at the largest, below the
+// rounding of a 16-bit weight).
+constexpr float kLeastCap = 1.f / 1024.f, kMostCap = 1024.f;
 // mods within their documented ranges
 inline bool mods_ok(const kv_score_mods* m) {
-    return m && m->softcap >= 0.f && m->softcap <= 3.4e38f && m->window >= 0 &&
+    return m && (m->softcap == 0.f || (m->softcap >= kLeastCap && m->softcap <= kMostCap)) &&
+           m->window >= 0 &&
            !(reinterpret_cast<uintptr_t>(m->alibi_slopes) & 3u) &&
            !(reinterpret_cast<uintptr_t>(m->first_visible) & 3u) &&
            !(reinterpret_cast<uintptr_t>(m->prefix_lens) & 3u);

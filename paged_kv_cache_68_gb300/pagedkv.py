@@ -512,6 +512,8 @@ class KVPool:
         self._h = self.handle.value
         self._ws: Optional[torch.Tensor] = None
         self._scored_need = {}                  # workspace bytes by (batch, query heads)
+        self._ws_scored: Optional[torch.Tensor] = None
+        self._ws_outgrown = []
 
     def close(self) -> None:
         if self.handle is not None:
@@ -595,9 +597,12 @@ class KVPool:
         if need is None:
             need = paged_attention_scored_workspace_size(self.handle, batch, num_q_heads)
             self._scored_need[batch, num_q_heads] = need
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_pool.device)
-        return self._ws
+        if self._ws_scored is None or self._ws_scored.numel() < need:
+            # (one that a captured graph may hold is kept, not handed back)
+            if self._ws_scored is not None:
+                self._ws_outgrown.append(self._ws_scored)
+            self._ws_scored = torch.empty(need, dtype=torch.uint8, device=self.k_pool.device)
+        return self._ws_scored
 
     def decode_scored(self, q, block_tables, seq_lens, scale: float, *, softcap: float = 0.0,
                       alibi_slopes=None, window: int = 0, first_visible=None, out=None,
