@@ -30,7 +30,6 @@ namespace pagedkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBigThreads = 512;          // many rows: 16 warps, a block's heads at once
 constexpr int kD = 128;
 constexpr int kMaxRows = 256;             // the largest block size
 constexpr int kHeld = 8;                  // row pairs a warp keeps in registers
@@ -62,27 +61,21 @@ template <> __device__ __forceinline__ float2 widen<__nv_bfloat16>(uint32_t w) {
 template <typename T> constexpr uint32_t kInfBits = 0x7c00u;
 template <> constexpr uint32_t kInfBits<__nv_bfloat16> = 0x7f80u;
 
-// The INT8 code of y in the low byte: clamped to [-127, 127], then rounded to
-// nearest even by the addition of 1.5 * 2^23, whose sum holds the integer in its
-// low bits (an FMA-pipe step; a conversion instruction takes the MUFU's, at an
-// eighth of the rate).
-__device__ __forceinline__ uint32_t int8_bits(float y) {
-    return __float_as_uint(__fadd_rn(fminf(fmaxf(y, -127.f), 127.f), 12582912.f));
-}
-
-// Q of two values: the low 16 bits hold their codes.
-template <bool INT8> __device__ __forceinline__ uint32_t encode2(float a, float b) {
-    if constexpr (INT8) return __byte_perm(int8_bits(a), int8_bits(b), 0x0040) & 0xffffu;
-    else return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-// Q of four, one word.
-template <bool INT8>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-    if constexpr (INT8)
-        return __byte_perm(__byte_perm(int8_bits(a), int8_bits(b), 0x0040),
-                           __byte_perm(int8_bits(c), int8_bits(d), 0x0040), 0x5410);
-    else
-        return encode2<false>(a, b) | (encode2<false>(c, d) << 16);
+// Q of four values, one word.  INT8: rounded to nearest even by the addition of
+// 1.5 * 2^23, whose sum holds the integer in its low byte (an FMA-pipe step; a
+// conversion instruction takes the MUFU's pipe, at an eighth of the rate; the
+// packed addition is not used: the compiler fused it with the product before it,
+// which must be rounded first).  No clamp: |x| (1 / new) is at most 127 (1 + 2^-22), and a factor below 1
+// only shrinks a code, so every sum rounds within [-127, 127].
+template <bool INT8> __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
+    if constexpr (INT8) {
+        auto bits = [](float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); };
+        return __byte_perm(__byte_perm(bits(a.x), bits(a.y), 0x0040),
+                           __byte_perm(bits(b.x), bits(b.y), 0x0040), 0x5410);
+    } else {
+        return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+               ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
+    }
 }
 
 // Four codes, each rounded again after a factor.
@@ -101,8 +94,9 @@ template <bool INT8> __device__ __forceinline__ uint32_t rescale4(uint32_t w, fl
             v[2 * i + 1] = x.y;
         }
     }
-    return encode4<INT8>(__fmul_rn(v[0], f), __fmul_rn(v[1], f), __fmul_rn(v[2], f),
-                         __fmul_rn(v[3], f));
+    const float2 f2 = make_float2(f, f);
+    return encode4<INT8>(__fmul2_rn(make_float2(v[0], v[1]), f2),
+                         __fmul2_rn(make_float2(v[2], v[3]), f2));
 }
 
 __global__ void __launch_bounds__(kThreads) mark_rows_kernel(const BlockAppend p) {
@@ -203,8 +197,7 @@ __device__ __forceinline__ void quantise_head(const BlockAppend& p, int part, in
             const float2 i2 = make_float2(inv, inv);
             const float2 f0 = __fmul2_rn(widen<T>(w[k].x), i2), f1 = __fmul2_rn(widen<T>(w[k].y), i2);
             const float2 f2 = __fmul2_rn(widen<T>(w[k].z), i2), f3 = __fmul2_rn(widen<T>(w[k].w), i2);
-            const uint2 c = make_uint2(encode4<INT8>(f0.x, f0.y, f1.x, f1.y),
-                                       encode4<INT8>(f2.x, f2.y, f3.x, f3.y));
+            const uint2 c = make_uint2(encode4<INT8>(f0, f1), encode4<INT8>(f2, f3));
             if (n < nw)
                 *reinterpret_cast<uint2*>(base + rows[n] * row_bytes + hl * 8) =
                     INT8 && now != now ? make_uint2(0u, 0u) : c;
@@ -213,25 +206,17 @@ __device__ __forceinline__ void quantise_head(const BlockAppend& p, int part, in
     if (lane == 0) *scale = now;
 }
 
-// The block's rows in `tok` (complete for every thread), by all warps of the CTA.
-template <typename T, bool INT8>
-__device__ __forceinline__ void quantise_block(const BlockAppend& p, int blk, const int* tok,
-                                               unsigned char* rows, int* nw_s) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) {
-        int n = 0;
-        for (int r0 = 0; r0 < p.bs; r0 += 32) {
-            const bool has = r0 + lane < p.bs && tok[r0 + lane] != 0;
-            const unsigned m = __ballot_sync(kAll, has);
-            if (has) rows[n + __popc(m & ((1u << lane) - 1u))] = (unsigned char)(r0 + lane);
-            n += __popc(m);
-        }
-        if (lane == 0) *nw_s = n;
+// The rows that `tok` has, in order, by one warp: how many.
+__device__ __forceinline__ int list_rows(const BlockAppend& p, const int* tok, unsigned char* rows,
+                                         int lane) {
+    int n = 0;
+    for (int r0 = 0; r0 < p.bs; r0 += 32) {
+        const bool has = r0 + lane < p.bs && tok[r0 + lane] != 0;
+        const unsigned m = __ballot_sync(kAll, has);
+        if (has) rows[n + __popc(m & ((1u << lane) - 1u))] = (unsigned char)(r0 + lane);
+        n += __popc(m);
     }
-    __syncthreads();
-    const int nw = *nw_s;
-    for (int item = warp; item < 2 * p.hkv; item += (int)(blockDim.x >> 5))
-        quantise_head<T, INT8>(p, item & 1, item >> 1, blk, tok, rows, nw, lane);
+    return n;
 }
 
 // Up to kScanTokens rows: a CTA per token, which reads all slots itself.
@@ -271,20 +256,32 @@ __global__ void __launch_bounds__(kThreads) append_scan_kernel(const BlockAppend
         }
     }
     if (__syncthreads_or(later)) return;             // a later token leads
-    quantise_block<T, INT8>(p, blk, tok, rows, &nw_s);
+    const int warp = tid >> 5, lane = tid & 31;
+    if (warp == 0) {
+        const int n = list_rows(p, tok, rows, lane);
+        if (lane == 0) nw_s = n;
+    }
+    __syncthreads();
+    for (int item = warp; item < 2 * p.hkv; item += kThreads / 32)
+        quantise_head<T, INT8>(p, item & 1, item >> 1, blk, tok, rows, nw_s, lane);
 }
 
 // Any number, after mark_rows_kernel: a CTA per `chunk` tokens writes the blocks
-// that they lead.  (The chunk's leaders are found at once: one token a thread.)
+// that they lead.  The chunk's leaders are found at once, one token a thread, and
+// up to kTogether of their blocks are worked on together: a chunk where one
+// request's rows end and the next one's begin leads two, and taking them in turn
+// made those CTAs last twice as long as the others (36 k cycles of 42 k, while the
+// SMs were busy 22 k on average).
+constexpr int kTogether = 4;
 template <typename T, bool INT8>
-__global__ void __launch_bounds__(kBigThreads, 2) append_marked_kernel(const BlockAppend p) {
-    __shared__ int tok[kMaxRows];
-    __shared__ unsigned char rows[kMaxRows];
-    __shared__ int led[kBigThreads];
-    __shared__ int nw_s, led_n;
+__global__ void __launch_bounds__(kThreads, 4) append_marked_kernel(const BlockAppend p) {
+    __shared__ int tok[kTogether][kMaxRows];
+    __shared__ unsigned char rows[kTogether][kMaxRows];
+    __shared__ int led[kThreads];
+    __shared__ int nw_s[kTogether], led_n;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long i = (long long)blockIdx.x * p.chunk + tid;
     if (tid == 0) led_n = 0;
     __syncthreads();
@@ -299,15 +296,25 @@ __global__ void __launch_bounds__(kBigThreads, 2) append_marked_kernel(const Blo
         }
     }
     __syncthreads();
-    for (int k = 0; k < led_n; ++k) {
-        const int blk = led[k];
-        if (tid < p.bs) {
-            tok[tid] = p.owner[(size_t)blk * p.bs + tid];
-            p.owner[(size_t)blk * p.bs + tid] = 0;
+    for (int k0 = 0; k0 < led_n; k0 += kTogether) {
+        const int nk = min(kTogether, led_n - k0);
+        for (int x = tid; x < nk * p.bs; x += kThreads) {
+            const int k = x / p.bs, r = x - k * p.bs;
+            int* owner = p.owner + (size_t)led[k0 + k] * p.bs + r;
+            tok[k][r] = *owner;
+            *owner = 0;
         }
         __syncthreads();
-        quantise_block<T, INT8>(p, blk, tok, rows, &nw_s);
-        __syncthreads();                             // tok and rows before the next block's
+        if (warp < nk) {
+            const int n = list_rows(p, tok[warp], rows[warp], lane);
+            if (lane == 0) nw_s[warp] = n;
+        }
+        __syncthreads();
+        for (int item = warp; item < nk * 2 * p.hkv; item += kThreads / 32) {
+            const int k = item / (2 * p.hkv), h = item - k * 2 * p.hkv;
+            quantise_head<T, INT8>(p, h & 1, h >> 1, led[k0 + k], tok[k], rows[k], nw_s[k], lane);
+        }
+        __syncthreads();                             // tok and rows before the next blocks'
     }
 }
 
@@ -331,8 +338,7 @@ cudaError_t launch(const BlockAppend& call, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // as many tokens to a CTA as fill a block, when they come in order: then most
     // CTAs lead one
-    p.chunk = std::min(p.bs, kBigThreads);
-    cfg.blockDim = dim3(kBigThreads);
+    p.chunk = std::min(p.bs, kThreads);
     cfg.gridDim = dim3((unsigned)((p.num_tokens + p.chunk - 1) / p.chunk));
     return cudaLaunchKernelEx(&cfg, append_marked_kernel<T, INT8>, p);
 }

@@ -1,4 +1,4 @@
-// The calls of a captured-size step whose host cost shows (kv_plan_step,
+// The calls of a step whose host cost shows (kv_plan_step, kv_append,
 // paged_attention_decode_scored, paged_attention_prefill_scored) on torch tensors:
 // argument marshalling only, like the ctypes binding, but without its 10-20 us of
 // interpreter time around kernels of 6-12 us.  A call checks its tensors, takes
@@ -157,6 +157,24 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// append(handle, k_new, v_new, slot_mapping, stream) -> None; the caller has
+// compared the rows' type with the pool's
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        count(n, 5);
+        const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"),
+                         &slots = tensor(a[3], "slot_mapping");
+        const int device = k.is_cuda() ? (int)k.get_device() : -1;
+        if (slots.dim() < 1 || slots.size(0) > 2147483647) throw BadArgument("slot_mapping must be [tokens]");
+        const void* pk = address(k, "k_new", k.scalar_type(), device);
+        const void* pv = address(v, "v_new", k.scalar_type(), device);
+        const auto* ps = static_cast<int64_t*>(address(slots, "slot_mapping", at::kLong, device));
+        const kv_status st = kv_append(handle(a[0]), pk, pv, ps, (int)slots.size(0), stream_of(a[4], device));
+        if (st != KV_OK) return PyLong_FromLong(st);
+        Py_RETURN_NONE;
+    });
+}
+
 // out given, or a new tensor like q.
 at::Tensor result(PyObject* o, const at::Tensor& q, const char* name) {
     if (o == Py_None) return at::empty_like(q);
@@ -238,6 +256,7 @@ PyObject* prefill_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"plan_step", (PyCFunction)(void (*)(void))plan_step, METH_FASTCALL, nullptr},
+    {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"decode_scored", (PyCFunction)(void (*)(void))decode_scored, METH_FASTCALL, nullptr},
     {"prefill_scored", (PyCFunction)(void (*)(void))prefill_scored, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

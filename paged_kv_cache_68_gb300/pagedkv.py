@@ -12,8 +12,8 @@ The module-level functions carry the C names (``kv_pool_create``,
 ``paged_attention_decode_cascade``, ``paged_attention_prefill``,
 ``paged_attention_decode_noalloc``,
 ``kv_pool_get_error``, ``kv_pool_clear_error``, ``kv_pool_destroy``);
-``KVPool`` bundles them for convenience; its ``plan_step``, ``decode_scored`` and
-``prefill_scored`` go through a small Python module over the same C ABI
+``KVPool`` bundles them for convenience; its ``plan_step``, ``append``,
+``decode_scored`` and ``prefill_scored`` go through a small Python module over the same C ABI
 (``csrc/torch_binding.cpp``), which marshals their tensors without the
 interpreter time that ctypes costs beside a kernel of a few microseconds.
 """
@@ -548,7 +548,13 @@ class KVPool:
         return StepPlan._make(r)
 
     def append(self, k_new, v_new, slot_mapping, stream=None) -> None:
-        kv_append(self.handle, k_new, v_new, slot_mapping, self.dtype, stream)
+        if k_new.dtype != self.dtype:
+            raise ValueError(f"k_new must be {self.dtype}, got {k_new.dtype}")
+        if isinstance(stream, torch.cuda.Stream):
+            stream = stream.cuda_stream
+        r = _fast().append(self._h, k_new, v_new, slot_mapping, stream)
+        if r is not None:
+            raise PagedKVError(r, "kv_append")
 
     def copy_blocks(self, pairs, stream=None) -> None:
         copy_blocks(self.handle, pairs, stream)
