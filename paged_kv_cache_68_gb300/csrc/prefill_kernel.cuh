@@ -312,6 +312,10 @@ template <> struct H16<__half> {
     }
 };
 
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -435,7 +439,26 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     // keep the grid's own order.
     int b = blockIdx.z, g = blockIdx.y;
     int pt = (int)gridDim.x - 1 - (int)blockIdx.x;
-    if (p.batch <= kMaxRanked) {
+    if (p.batch <= 32) {
+        // every warp ranks the requests by itself: a lane each, no barrier
+        const int k = (int)(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
+        const int per_req = (int)(gridDim.x * gridDim.y);
+        const int rank = k / per_req, rem = k % per_req;
+        int cost = -1;
+        if (lane < p.batch) {
+            const int c0 = p.cu_seqlens[lane], c1 = p.cu_seqlens[lane + 1];
+            const int Li = min(p.seq_lens[lane], p.max_blocks * bs);
+            cost = (c1 > c0 && Li > 0) ? (Li + BN - 1) / BN : 0;
+        }
+        int above = 0;                             // requests ordered before this one
+        for (int o = 0; o < p.batch; ++o) {
+            const int co = __shfl_sync(FULL, cost, o);
+            above += co > cost || (co == cost && o < lane);
+        }
+        b = __ffs((int)__ballot_sync(FULL, lane < p.batch && above == rank)) - 1;
+        g = rem % (int)gridDim.y;
+        pt = (int)gridDim.x - 1 - rem / (int)gridDim.y;
+    } else if (p.batch <= kMaxRanked) {
         int* cost = reinterpret_cast<int*>(smem + LY::order);
         int* pick = cost + kMaxRanked;
         const int k = (int)(blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z));
@@ -478,38 +501,10 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
     const int nstreams = nqb > 0 ? 2 : 1;
     const int P0 = L - C + q0;                     // position of stream A's first query
     const int Pmax = P0 + (nstreams == 2 ? QT + nqb : nqa) - 1;   // the last query's (<= L - 1)
-    // every active stream walks all tiles (rows past their own limit are
-    // masked), so each K/V tile has exactly `nstreams` consumers
-    int ntiles = Pmax >= 0 ? Pmax / BN + 1 : 0;
-    int jt0 = 0;                                   // the first tile walked
-    int vbeg = 0, vend = L;                        // positions some query of the CTA sees
-    int prefix = 0;
-    if constexpr (MOD) {
-        prefix = p.prefix != nullptr ? p.prefix[b] : 0;
-        int* span = reinterpret_cast<int*>(smem + LY::order) + kMaxRanked + 1;   // lo, hi
-        if (tid == 0) {
-            span[0] = 0x7fffffff;
-            span[1] = -1;
-        }
-        __syncthreads();
-        if (tid < nqa + max(nqb, 0)) {
-            int lo, hi;
-            visible_range(p, P0 + tid, L, prefix, cu0 + q0 + tid, lo, hi);
-            if (lo <= hi) {
-                atomicMin(&span[0], lo);
-                atomicMax(&span[1], hi);
-            }
-        }
-        __syncthreads();
-        vbeg = span[0];
-        vend = span[1] + 1;
-        jt0 = vend > 0 ? vbeg / BN : 0;
-        ntiles = vend > 0 ? (vend - 1) / BN - jt0 + 1 : 0;
-    }
-
-    // -- set-up: barriers, TMEM ----------------------------------------------
-    if (tid == 0) {
-        for (int i = 0; i < LY::nbars; ++i) {
+    // -- set-up: barriers and the queries' copy (one warp), TMEM (another) ----
+    const bool load_q = Pmax >= 0;
+    if (warp == WARP_TMAK) {
+        for (int i = lane; i < LY::nbars; i += 32) {
             uint32_t count = 1;
             if ((i >= BAR_KE && i < BAR_KE + KST) || (i >= BAR_VE && i < BAR_VE + VST))
                 count = (uint32_t)nstreams;
@@ -526,8 +521,19 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
             if (i == BAR_QC) count = (uint32_t)(NSOFT * nstreams);   // each softmax warp its rows
             dec::mbar_init(bar(i), count);
         }
-        *abort_flag = 0;
+        if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        dec::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && load_q) {
+            dec::mbar_arrive_tx(bar(BAR_Q), (uint32_t)nstreams * QTILE);
+            for (int x = 0; x < nstreams; ++x) {
+                const uint32_t d = sbase + OFF_Q + (uint32_t)x * QTILE;
+                dec::tma_load_3d(d, &tmap_q, 0, g * G, cu0 + q0 + x * QT, bar(BAR_Q));
+                dec::tma_load_3d(d + QHALF, &tmap_q, 64, g * G, cu0 + q0 + x * QT, bar(BAR_Q));
+            }
+        }
+        __syncwarp();
     }
     if (warp == WMMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -536,6 +542,30 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+
+    // every active stream walks all tiles (rows past their own limit are
+    // masked), so each K/V tile has exactly `nstreams` consumers
+    int ntiles = Pmax >= 0 ? Pmax / BN + 1 : 0;
+    int jt0 = 0;                                   // the first tile walked
+    int vbeg = 0, vend = L;                        // positions some query of the CTA sees
+    int prefix = 0;
+    if constexpr (MOD) {
+        prefix = p.prefix != nullptr ? p.prefix[b] : 0;
+        int first = 0x7fffffff, last = -1;         // (every warp finds them by itself)
+        for (int i = lane; i < nqa + max(nqb, 0); i += 32) {
+            int lo, hi;
+            visible_range(p, P0 + i, L, prefix, cu0 + q0 + i, lo, hi);
+            if (lo <= hi) {
+                first = min(first, lo);
+                last = max(last, hi);
+            }
+        }
+        vbeg = __reduce_min_sync(FULL, first);
+        vend = __reduce_max_sync(FULL, last) + 1;
+        jt0 = vend > 0 ? vbeg / BN : 0;
+        ntiles = vend > 0 ? (vend - 1) / BN - jt0 + 1 : 0;
+    }
+
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -552,14 +582,6 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
         const int nbox = BN / R;                   // boxes per KV tile (<= 8)
         const uint32_t box_bytes = (uint32_t)R * 128u;   // one box, one 64-dim half
         if (ntiles > 0) {
-            if (is_k && lane == 0) {
-                dec::mbar_arrive_tx(bar(BAR_Q), (uint32_t)nstreams * QTILE);
-                for (int x = 0; x < nstreams; ++x) {
-                    const uint32_t d = sbase + OFF_Q + (uint32_t)x * QTILE;
-                    dec::tma_load_3d(d, &tmap_q, 0, g * G, cu0 + q0 + x * QT, bar(BAR_Q));
-                    dec::tma_load_3d(d + QHALF, &tmap_q, 64, g * G, cu0 + q0 + x * QT, bar(BAR_Q));
-                }
-            }
             const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
             if constexpr (Q8) {
                 // Tile jj's code rows land in code stage jj % CST (INT8: its
@@ -650,7 +672,7 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 // Drain: no copy may still be landing in shared memory at exit.
                 if (BLOCKSC) dec::cp_async_wait_all();
                 if (lane == 0) {
-                    bool ok = !is_k || dec::mbar_wait(bar(BAR_Q), 0);
+                    bool ok = true;
                     for (int jj = max(0, codes_issued - CST); jj < codes_issued; ++jj)
                         ok &= dec::mbar_wait(bar(cfull0 + jj % CST), (jj / CST) & 1);
                     if (!ok) atomicOr(p.err, KV_DEVERR_TIMEOUT);
@@ -688,13 +710,15 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                 }
                 // Drain: no copy may still be landing in shared memory at exit.
                 if (lane == 0) {
-                    bool ok = !is_k || dec::mbar_wait(bar(BAR_Q), 0);
+                    bool ok = true;
                     for (int j = max(0, issued - nst); j < issued; ++j)
                         ok &= dec::mbar_wait(bar(full0 + j % nst), (j / nst) & 1);
                     if (!ok) atomicOr(p.err, KV_DEVERR_TIMEOUT);
                 }
             }
         }
+        if (is_k && load_q && lane == 0 && !dec::mbar_wait(bar(BAR_Q), 0))
+            atomicOr(p.err, KV_DEVERR_TIMEOUT);
     } else if (Q8 && (warp == WARP_CVK || warp == WARP_CVV)) {
       if constexpr (Q8) {
         // ------------------------------------- helper converters (8-bit) ----
@@ -838,16 +862,23 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                         return reinterpret_cast<uint4*>(qt + (c >> 3) * QHALF + r * 128 +
                                                         (((c & 7) ^ (r & 7)) << 4));
                     };
-                    float amax = 0.f;
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        const uint4 w = *chunk(c);
-                        const uint32_t e4[4] = {w.x, w.y, w.z, w.w};
+                    uint4 w[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            amax = fmaxf(amax, fmaxf(fabsf(H16<T>::low(e4[e])),
-                                                     fabsf(H16<T>::high(e4[e]))));
+                    for (int c = 0; c < 16; ++c) w[c] = *chunk(c);
+                    // (the largest |q|, two at a time: 16-bit maxima are exact)
+                    __nv_bfloat162 mx[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = __float2bfloat162_rn(0.f);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        mx[0] = __hmax2(mx[0], __habs2(as_bf162(w[c].x)));
+                        mx[1] = __hmax2(mx[1], __habs2(as_bf162(w[c].y)));
+                        mx[2] = __hmax2(mx[2], __habs2(as_bf162(w[c].z)));
+                        mx[3] = __hmax2(mx[3], __habs2(as_bf162(w[c].w)));
                     }
+                    const float2 mf = __bfloat1622float2(
+                        __hmax2(__hmax2(mx[0], mx[1]), __hmax2(mx[2], mx[3])));
+                    const float amax = fmaxf(mf.x, mf.y);
                     // 2^e with amax * 2^e in [2^14, 2^15): the exponent field of amax
                     int ex2 = 0;
                     if (amax > 0.f && amax <= 3.0e38f) {
@@ -855,16 +886,14 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
                         ex2 = min(max(15 - ex, -120), 120);
                     }
                     const float up = __uint_as_float((uint32_t)(ex2 + 127) << 23);
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        const uint4 w = *chunk(c);
-                        uint32_t e4[4] = {w.x, w.y, w.z, w.w};
+                    auto conv = [&](uint32_t q2) {
+                        const float2 y = __fmul2_rn(make_float2(H16<T>::low(q2), H16<T>::high(q2)),
+                                                    make_float2(up, up));
+                        return H16<__half>::pack(y.x, y.y);
+                    };
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            e4[e] = H16<__half>::pack(H16<T>::low(e4[e]) * up,
-                                                      H16<T>::high(e4[e]) * up);
-                        *chunk(c) = make_uint4(e4[0], e4[1], e4[2], e4[3]);
-                    }
+                    for (int c = 0; c < 16; ++c)
+                        *chunk(c) = make_uint4(conv(w[c].x), conv(w[c].y), conv(w[c].z), conv(w[c].w));
                     qs *= __uint_as_float((uint32_t)(127 - ex2) << 23);
                     dec::fence_proxy_async();
                     __syncwarp();
@@ -1097,26 +1126,43 @@ __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
         const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         const bool done = have_o || (ok && ntiles == 0);
         const float inv = l > 0.f ? p.vscale / l : 0.f;   // FP8: the pool's V scale
-        T* orow = static_cast<T*>(p.out) +
-                  ((size_t)(cu0 + q0 + x * QT + qi) * p.num_q_heads + (size_t)g * G + hh) * D;
+        // Through the stream's query tile, which every product has read: a warp
+        // writes its 32 rows there (its own, swizzled) and stores whole rows, 16
+        // lanes each.  Storing straight from the lanes, a row each, touched 32
+        // lines an instruction and cost 2 us at the end of every CTA.
+        unsigned char* stage = smem + OFF_Q + (uint32_t)x * QTILE;
+        auto chunk_of = [&](int row, int c) {
+            return reinterpret_cast<uint4*>(stage + (c >> 3) * QHALF + row * 128 +
+                                            (((c & 7) ^ (row & 7)) << 4));
+        };
+        if (have_o) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t ov[32];
-            if (have_o) {
+            for (int c = 0; c < 4; ++c) {
+                uint32_t ov[32], w[16];
                 tmem_ld32(trow + COL_O + 32u * c, ov);
                 tmem_wait_ld();
-            }
-            if (valid && done) {
-                uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    w[e] = have_o && (!MOD || l > 0.f) ? H16<T>::pack(__uint_as_float(ov[2 * e]) * inv,
-                                                 __uint_as_float(ov[2 * e + 1]) * inv)
-                                  : 0u;
-                uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+                    w[e] = !MOD || l > 0.f ? H16<T>::pack(__uint_as_float(ov[2 * e]) * inv,
+                                                          __uint_as_float(ov[2 * e + 1]) * inv)
+                                           : 0u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    *chunk_of(r, 4 * c + e) =
+                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
+            __syncwarp();
+        }
+        if (done) {
+            T* out = static_cast<T*>(p.out) +
+                     ((size_t)(cu0 + q0 + x * QT) * p.num_q_heads + (size_t)g * G) * D + (lane & 15) * 8;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int row = 32 * qd + 2 * i + (lane >> 4);
+                if (row / G < nq)
+                    *reinterpret_cast<uint4*>(
+                        out + ((size_t)(row / G) * p.num_q_heads + row % G) * D) =
+                        have_o ? *chunk_of(row, lane & 15) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
