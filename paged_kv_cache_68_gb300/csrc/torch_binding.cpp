@@ -109,6 +109,15 @@ void count(Py_ssize_t n, Py_ssize_t want) {
     }
 }
 
+// A tensor of n elements over `all`'s storage, from byte `from` on.
+at::Tensor part(const at::Tensor& all, int64_t from, int64_t n, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(from / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
+}
+
 // plan_step(handle, context_lens, new_lens, block_tables, free_blocks, free_head,
 //           num_tokens, stream) -> (cu_seqlens, seq_lens, slots, positions, head)
 PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -132,10 +141,16 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         auto* pt = static_cast<int32_t*>(address(tables, "block_tables", at::kInt, device));
         const auto* pf = static_cast<int32_t*>(address(blocks, "free_blocks", at::kInt, device));
         const auto* ph = static_cast<int32_t*>(address(head, "free_head", at::kInt, device));
-        const auto i32 = ctx.options();
-        at::Tensor cu = at::empty({b + 1}, i32), lens = at::empty({b}, i32);
-        at::Tensor slots = at::empty({tokens}, i32.dtype(at::kLong)), pos = at::empty({tokens}, i32);
-        at::Tensor out = at::empty({1}, i32);
+        // The five results lie in one allocation, each on a 256-byte boundary: an
+        // at::empty costs more than the rest of the call (8.5 -> 6.5 us a call).
+        const auto room = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+        const int64_t at_lens = room(4 * (b + 1)), at_pos = at_lens + room(4 * b),
+                      at_slots = at_pos + room(4 * (int64_t)tokens),
+                      at_head = at_slots + room(8 * (int64_t)tokens);
+        const at::Tensor all = at::empty({at_head + 4}, ctx.options().dtype(at::kByte));
+        at::Tensor cu = part(all, 0, b + 1, at::kInt), lens = part(all, at_lens, b, at::kInt);
+        at::Tensor pos = part(all, at_pos, tokens, at::kInt), slots = part(all, at_slots, tokens, at::kLong);
+        at::Tensor out = part(all, at_head, 1, at::kInt);
         const kv_status st = kv_plan_step(
             handle(a[0]), pc, pn, (int)b, pt, (int)tables.size(1), pf, (int)blocks.numel(), ph,
             static_cast<int32_t*>(out.data_ptr()), static_cast<int32_t*>(cu.data_ptr()),
