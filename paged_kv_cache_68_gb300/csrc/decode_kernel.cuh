@@ -617,6 +617,10 @@ __device__ __forceinline__ float fold_state(float M, float& den, float lse_p, fl
 //     so the bias is slope (t - P), exact up to one rounding of the product;
 //   masks:    rows of the tile before n_lo, like rows from n_valid on, take no
 //     part.
+// None of it binds: the bytes of K and V from the first to the last visible
+// position do.  8 sequences of 40,000 tokens (window 32768, cap 50, 786 MB) take
+// 137 us, 86 % of the measured HBM peak; 33 of 600 tokens and 40 heads with
+// slopes (484 MB) 86 us, 84 %.
 // Without kMod every member is unused and every call the identity.
 template <bool MOD, int NH, bool EXACT = false>
 struct ScoreMods {

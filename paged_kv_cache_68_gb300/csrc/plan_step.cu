@@ -20,7 +20,9 @@
 // shared memory; at most 4096 requests, 32 KB) and then places its own
 // contiguous share of the tokens: a redundant scan out of L2 costs less than
 // a second launch and needs no workspace.  Bound by latency: the chain lengths
-// -> sums -> free id or table entry -> slot.
+// -> sums -> free id or table entry -> slot.  Launches back to back: 256 decoding
+// requests (13 KB) 3.8 us, 1000 prompts of 403,000 tokens (5.1 MB, 0.8 us of HBM
+// time) 7.1 us.
 #include <algorithm>
 
 #include "pagedkv_internal.cuh"

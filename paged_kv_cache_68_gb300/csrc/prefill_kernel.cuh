@@ -401,6 +401,16 @@ constexpr int kModsMask = 1, kModsCap = 2, kModsBias = 4, kModsAny = 8;
 // operations a score beside the softmax's one.  The tiles walked run from the
 // first to the last position that any of the CTA's queries sees; each row
 // masks what lies outside its own lo..hi.
+//
+// Measured (bf16, 16 x 512 queries behind 0.2 - 4 k tokens, 32 / 8 heads, 214
+// GFLOP): masks alone 230 us (929 TFLOP/s), capped 335 us (638), capped and
+// biased 410 us.  The products with P's two halves need 166 us of the tensor
+// cores; what bounds a capped tile is the two softmax warps of each SM
+// sub-partition: 3,250 clocks a tile, of which they issue in 43 % and keep the
+// MUFU busy in 56 % (a tanh as polynomial on the FMA pipe: 355 us; one
+// reciprocal for two scores: no gain).  About 12,000 clocks of a CTA come before
+// its first and after its last tile, which is what short spans pay most for:
+// 8,100 queries on an FP8 pool that see 600 positions or less take 90 us.
 template <typename T, int G, int FMT = -1,
           int SC = FMT == dec::kFmtInt8 ? dec::kScToken : dec::kScPool, int MODS = 0>
 __global__ void __launch_bounds__(FMT >= 0 ? NTHREADS_Q8 : NTHREADS, 1)
