@@ -172,19 +172,23 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// append(handle, k_new, v_new, slot_mapping, stream) -> None; the caller has
-// compared the rows' type with the pool's
+// append(handle, k_new, v_new, slot_mapping, row, stream) -> None; row: elements of
+// a token's K or V; the caller has compared the rows' type with the pool's
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        count(n, 5);
+        count(n, 6);
         const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"),
                          &slots = tensor(a[3], "slot_mapping");
         const int device = k.is_cuda() ? (int)k.get_device() : -1;
         if (slots.dim() < 1 || slots.size(0) > 2147483647) throw BadArgument("slot_mapping must be [tokens]");
+        const int64_t need = slots.size(0) * (int64_t)small(a[4], "row");
+        if (k.numel() < need || v.numel() < need)
+            throw BadArgument("k_new and v_new must hold a row for each of the " +
+                              std::to_string(slots.size(0)) + " slots");
         const void* pk = address(k, "k_new", k.scalar_type(), device);
         const void* pv = address(v, "v_new", k.scalar_type(), device);
         const auto* ps = static_cast<int64_t*>(address(slots, "slot_mapping", at::kLong, device));
-        const kv_status st = kv_append(handle(a[0]), pk, pv, ps, (int)slots.size(0), stream_of(a[4], device));
+        const kv_status st = kv_append(handle(a[0]), pk, pv, ps, (int)slots.size(0), stream_of(a[5], device));
         if (st != KV_OK) return PyLong_FromLong(st);
         Py_RETURN_NONE;
     });

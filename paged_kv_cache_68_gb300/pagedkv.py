@@ -510,6 +510,7 @@ class KVPool:
             self.handle = kv_pool_create_quantized(k_pool, v_pool, dtype, cache, k_scales,
                                                    v_scales, k_scale, v_scale)
         self._h = self.handle.value
+        self._row = self.num_kv_heads * self.head_dim
         self._ws: Optional[torch.Tensor] = None
         self._scored_need = {}                  # workspace bytes by (batch, query heads)
         self._ws_scored: Optional[torch.Tensor] = None
@@ -552,7 +553,7 @@ class KVPool:
             raise ValueError(f"k_new must be {self.dtype}, got {k_new.dtype}")
         if isinstance(stream, torch.cuda.Stream):
             stream = stream.cuda_stream
-        r = _fast().append(self._h, k_new, v_new, slot_mapping, stream)
+        r = _fast().append(self._h, k_new, v_new, slot_mapping, self._row, stream)
         if r is not None:
             raise PagedKVError(r, "kv_append")
 

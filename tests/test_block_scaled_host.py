@@ -160,3 +160,18 @@ def test_the_python_module_refuses_wrong_tensors():
         for k, bad in bads + ((1, q),):
             with pytest.raises(ValueError):
                 fn(*[bad if n == k else a for n, a in enumerate(good)])
+
+
+def test_append_refuses_fewer_rows_than_slots():
+    """Rows that would be read past their end are refused before any call."""
+    from paged_kv_cache_68_gb300 import pagedkv
+    m = pagedkv._fast()
+    rows, slots = torch.zeros(3, 2, 128, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int64)
+    full = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    for k, v in ((rows, full), (full, rows)):
+        with pytest.raises(ValueError, match="a row for each of the 4 slots"):
+            m.append(0, k, v, slots, 256, None)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        m.append(0, full, full, slots, 256, None)
+    with pytest.raises(TypeError):
+        m.append(0, full, full, slots, 256)
