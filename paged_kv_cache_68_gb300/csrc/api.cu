@@ -362,17 +362,23 @@ static kv_status finish_pool(kv_pool* p, kv_pool_t* out) {
     cudaError_t e = cudaGetDevice(&p->device);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
+    // Zeroed before the handle is out: a memset queued on the default stream need
+    // not have run when another, non-blocking stream makes the first call.
+    cudaStream_t zero = nullptr;
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&zero, cudaStreamNonBlocking);
     if (e == cudaSuccess) e = cudaMalloc(&p->d_err, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(p->d_err, 0, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemsetAsync(p->d_err, 0, sizeof(int), zero);
     if (e == cudaSuccess && p->block_scales) {
         const size_t rows = (size_t)p->num_blocks * p->block_size;
         const size_t bytes = sizeof(int) * (rows + p->num_blocks);
         e = cudaMalloc(&p->d_owner, bytes);
         if (e == cudaSuccess) {
             p->d_leader = p->d_owner + rows;
-            e = cudaMemset(p->d_owner, 0, bytes);
+            e = cudaMemsetAsync(p->d_owner, 0, bytes, zero);
         }
     }
+    if (e == cudaSuccess) e = cudaStreamSynchronize(zero);
+    if (zero) cudaStreamDestroy(zero);
     if (e != cudaSuccess) {
         cudaFree(p->d_err);
         cudaFree(p->d_owner);

@@ -223,3 +223,34 @@ def test_append_of_infinities_into_a_block_of_zeros():
         assert float(dsc[0]) == 0.0
     finally:
         pool.close()
+
+
+def test_first_append_on_another_stream_than_the_pool_was_made_on():
+    """A new pool's notes are zero for any stream, however busy the stream it was
+    made on is."""
+    n, bs, h, t = 2000, 16, 2, 3000
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn((t, h, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    slots = torch.arange(5, 5 + t, device="cuda")
+    busy = torch.randn((4096, 4096), device="cuda")
+    res = []
+    for other in (False, True):
+        codes = [torch.zeros((n, bs, h, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        sc = [torch.zeros((n, h), device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        if other:
+            for _ in range(20):
+                busy = busy @ busy * 1e-3
+        pool = pagedkv.KVPool(*codes, cache="fp8_e4m3", dtype=torch.bfloat16, k_scales=sc[0],
+                              v_scales=sc[1], scale_per="block")
+        try:
+            stream = torch.cuda.Stream() if other else None
+            for _ in range(2):
+                pool.append(k, v, slots, stream=stream)
+            torch.cuda.synchronize()
+            assert pool.get_error() == 0
+        finally:
+            pool.close()
+        res.append(codes + sc)
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
